@@ -448,6 +448,148 @@ int zero_gather_params(const uint16_t* const* windows, int32_t nd, int64_t part,
 int zero_gather_layers(const uint16_t* const* windows, int32_t nd, int64_t part, const int64_t* ranges,
                        int32_t nranges, uint16_t* const* dsts, void* stream);
 
+/* ---- tensor lists -----------------------------------------------------
+ * The optimizer step of parameters that are separate tensors (stage 0, or
+ * the tensors and fragments that zero_plan_partitions gives a rank) rather
+ * than one flat window: one launch steps the whole list, in place.  Sources
+ * as for the fused step: mixed-precision Adam with float32 master weights,
+ * momentum and variance (anthology note "Assumptions"; trishampatil "The
+ * Real Problem").  The 8-bit states are this library's own; the pages hold
+ * K = 12 bytes only.
+ *
+ * A list's tensors share three types:
+ *   grad_type   ZERO_TYPE_F32, F16 or BF16;
+ *   param_type  F16 or BF16 for a 16-bit copy of the weights that each step
+ *               writes (RNE of the new master), ZERO_TYPE_NONE for none;
+ *   state_type  ZERO_TYPE_F32, or ZERO_TYPE_MX8 for states in 8 bits, or
+ *               ZERO_TYPE_NONE for a list of gradients alone (norms).
+ *
+ * ZERO_TYPE_MX8 holds the momentum, and the square root of the variance,
+ * as microscaled blocks: 32 consecutive elements (counted from the tensor's
+ * first; the last block may be short) share one scale byte e that stands
+ * for 2^(e - 127), and each element is one e4m3 code (OCP FP8: 4 exponent
+ * bits, 3 mantissa bits, largest finite value 448).  An encoded block has
+ * the smallest e >= 1 that keeps its largest magnitude within 448 scales;
+ * a block that holds an inf or a NaN has e = 255 and every code NaN.  A
+ * positive root keeps at least the smallest positive code, since a root of
+ * 0 would turn the next update into m / eps.
+ *
+ * Rounding of 8-bit states: ZERO_ROUND_NEAREST (ties to even), or
+ * ZERO_ROUND_STOCHASTIC, which rounds up with the probability of the part
+ * that is cut off (in steps of 2^-20).  With beta2 = 0.999 a step changes a
+ * variance by about a thousandth, far less than half a step of an e4m3
+ * root, so that nearest rounding leaves it where it is; stochastic rounding
+ * moves it right on average.  The random word of element i is
+ *   mix(c ^ k1, k2),  c = (flat_off + i) mod 2^32,
+ *   k1 = mix(lo(seed) ^ mix(hi(seed) ^ mix(step, 0), 0), 0),  k2 = mix(~k1, 0),
+ *   mix(x, k): x ^= x >> 16; x *= 0xACE5F457; x ^= (x >> 15) ^ k;
+ *              x *= 0x7B639EB3; x ^= x >> 16        (modulo 2^32),
+ * step the number of the step taken (t + 1); the momentum takes the word's
+ * top 20 bits, the root its low 16 bits with four zeros behind.  Elements
+ * 2^32 apart share their word.
+ */
+#define ZERO_TYPE_NONE 0
+#define ZERO_TYPE_F32  1
+#define ZERO_TYPE_F16  2
+#define ZERO_TYPE_BF16 3
+#define ZERO_TYPE_MX8  4
+#define ZERO_ROUND_NEAREST    0
+#define ZERO_ROUND_STOCHASTIC 1
+
+/* One tensor: n contiguous elements of each array, device memory, aligned to
+ * its elements (no more is needed; arrays on 16-byte boundaries are
+ * fastest).  A tensor with n == 0 is valid and its pointers are ignored. */
+typedef struct zero_tensor {
+    float* master;       /* fp32 weights, updated in place */
+    const void* grad;    /* gradient, of grad_type */
+    void* param;         /* 16-bit copy, of param_type; NULL with ZERO_TYPE_NONE */
+    void* exp_avg;       /* momentum: float[n], or n codes */
+    void* exp_avg_sq;    /* variance: float[n], or n codes of its root */
+    uint8_t* avg_scale;  /* ZERO_TYPE_MX8: ceil(n / 32) scale bytes; else NULL */
+    uint8_t* sq_scale;
+    int64_t n;           /* >= 0 */
+    int64_t flat_off;    /* >= 0: first counter of the random words (for a fragment, its flat_off) */
+    int64_t reserved;    /* must be 0 */
+} zero_tensor;
+
+/* What the calls need to know of a planned list (host). */
+typedef struct zero_tensor_list {
+    int32_t n_tensors, grad_type, param_type, state_type;
+    int64_t n_elems;
+    int64_t n_chunks;     /* units of work: at most 4096 elements of one tensor each */
+    int64_t table_bytes;  /* bytes of the table */
+    int64_t reserved;     /* must be 0 */
+} zero_tensor_list;
+
+/* Validates a list (host, synchronous) and writes its table, table_bytes
+ * bytes that hold every pointer and the units of work; the caller copies it
+ * to 16-byte aligned device memory and passes that address, with *list, to
+ * the calls below, for as long as the tensors stay where they are.  Planned
+ * again when one moves.
+ *   table: host, 16-byte aligned, table_cap bytes; may be NULL if table_cap
+ *     is 0.  If the table needs more the call returns ZERO_ECAPACITY after
+ *     filling *list (call again with table_bytes bytes).
+ * No array that a step writes may overlap any other array of the list;
+ * gradients may overlap each other.  With ZERO_TYPE_NONE states only `grad`
+ * is looked at.  (No call can see whether a control block, flag, sum or
+ * workspace overlaps a list's tensors: they must not.)
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW, ZERO_ECAPACITY, ZERO_EALIAS.
+ */
+int zero_tensors_plan(const zero_tensor* tensors, int32_t n_tensors, int32_t grad_type, int32_t param_type,
+                      int32_t state_type, zero_tensor_list* list, void* table, int64_t table_cap);
+
+/* *sumsq = sum over the list of g^2 with g = raw * (1/L), in float64 in a
+ * fixed order (the same list gives the same bits on the same GPU), and
+ * *overflow = 1 if that sum is inf or NaN, as it is with any inf or NaN
+ * gradient or a scale without a finite reciprocal, else 0.  One launch.  An
+ * empty list gives 0 and 0.
+ *   loss_scale: L, ignored if ctl is not NULL; then L = ctl->loss_scale
+ *     (dynamic loss scaling).
+ *   overflow, sumsq: device, as in zero_reduce_owned.  Where ranks hold
+ *     parts of the parameters, the flags are OR-ed and the sums added across
+ *     them before the step.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EALIAS, ZERO_EHIP.
+ */
+int zero_tensors_grad_norm(const zero_tensor_list* list, const void* table, double loss_scale,
+                           const zero_step_ctl* ctl, int32_t* overflow, double* sumsq, void* workspace,
+                           void* stream);
+
+/* One Adam/AdamW step of every tensor of the list, in place, in one launch:
+ * the float64 sequence of zero_adam_step on g = raw * (coef / L), m', v' and
+ * p' rounded to fp32; with 8-bit states fp32(m') and the fp32 square root
+ * of fp32(v') are then encoded (zero_mx8_encode), and read back as
+ * zero_mx8_decode does.  The step number and the beta powers are ctl's; the
+ * launch's last workgroup commits the step there (t += 1; `cur` is not
+ * used).
+ *   overflow: device flag of zero_tensors_grad_norm; nonzero skips the step:
+ *     no tensor is touched, ctl->skipped += 1, the dynamic scale backs off.
+ *     NULL: the step is always taken, and an inf or NaN gradient reaches its
+ *     own element (and with 8-bit states its block).
+ *   sumsq: device sum; recorded in ctl->sumsq.  hp->max_grad_norm > 0
+ *     (needs both) gives coef = min(1, max_grad_norm / (sqrt(*sumsq) + 1e-6)),
+ *     else coef = 1.
+ *   hp->scale_interval > 0 (needs overflow): L = ctl->loss_scale and the
+ *     commit advances it, as in zero_adam_step; else L = loss_scale.
+ *   rounding, seed: of 8-bit states; ZERO_ROUND_NEAREST with fp32 states.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EALIAS, ZERO_EHIP.
+ */
+int zero_tensors_adam_step(const zero_tensor_list* list, const void* table, const zero_adam_hp* hp,
+                           double loss_scale, zero_step_ctl* ctl, const int32_t* overflow, const double* sumsq,
+                           int32_t rounding, uint64_t seed, void* workspace, void* stream);
+
+/* One array into the 8-bit form and back: codes[n] and ceil(n / 32) scales.
+ * root = 0: values (a momentum); root = 1: encode takes the square root of x
+ * first (a variance; a negative x makes its block NaN) and decode squares.
+ * step, flat_off: of the random words (ZERO_ROUND_STOCHASTIC).  Encoding is
+ * what a step does with its new state, bit for bit.  Decode takes any scale
+ * byte (0 is 2^-127, 255 NaN).  x: device, 4-byte aligned; no two of the
+ * arrays may overlap.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW, ZERO_EALIAS, ZERO_EHIP.
+ */
+int zero_mx8_encode(const float* x, int64_t n, int32_t root, uint8_t* codes, uint8_t* scales, int32_t rounding,
+                    uint64_t seed, int64_t step, int64_t flat_off, void* stream);
+int zero_mx8_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, int32_t root, float* x, void* stream);
+
 /* ---- emit (all-gather half) ------------------------------------------
  * allgather[allgather_off + j] = fp16_RNE(master[j]) for j < n (IEEE
  * round-to-nearest-even, overflow to inf).  Initial fill of the all-gather

@@ -1,0 +1,665 @@
+"""The tensor-list operators on the GPU against the oracle (float64
+arithmetic, fp32 or 8-bit storage).
+
+Weights and states are compared bit for bit: both sides take the same IEEE
+float64 operations in the same order and round once (RNE) to fp32, and the
+8-bit form is defined to the last bit.  The sum of squares is compared
+within 64 * 2^-53 relative: at these sizes a sum of non-negative terms
+passes at most 16 additions in a lane, 9 in its workgroup, 8 + 9 over the
+workgroups' parts and 2 products, each off by at most 2^-53 relative.
+"""
+import numpy as np
+import pytest
+
+from oracle import tensor_oracle as to
+
+from gpu_util import torch_mod
+
+pytestmark = pytest.mark.gpu
+
+F32, U8 = np.float32, np.uint8
+GRADS = {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}
+CANARY = 0xA5
+
+
+def bits(x):
+    """A device tensor's bytes as unsigned integers of its element's width."""
+    torch = torch_mod()
+    kind = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[x.element_size()]
+    a = x.contiguous().view(kind).cpu().numpy()
+    return a.view({1: np.uint8, 2: np.uint16, 4: np.uint32}[x.element_size()])
+
+
+def as_grad(values, kind):
+    """(device values, host array as the oracle takes it) of float values."""
+    torch = torch_mod()
+    t = torch.from_numpy(np.asarray(values, dtype=F32)).to(getattr(torch, GRADS[kind]))
+    host = t.view(torch.int16).numpy().view(np.uint16) if kind == "bf16" else t.numpy()
+    return t, host
+
+
+class Arena:
+    """Tensors packed with odd gaps in one buffer of canary bytes: every
+    tensor starts at its element's own alignment and at no better one."""
+
+    def __init__(self, nbytes):
+        torch = torch_mod()
+        self.buf = torch.full((nbytes,), CANARY, dtype=torch.uint8, device="cuda")
+        self.at, self.used = 0, np.zeros(nbytes, dtype=bool)
+
+    def take(self, n, dtype, skew=1):
+        torch = torch_mod()
+        size = torch.empty(0, dtype=dtype).element_size()
+        start = (self.at + 16 + 15) // 16 * 16 + skew * size
+        end = start + n * size
+        assert end + 16 <= self.buf.numel()
+        self.used[start:end] = True
+        self.at = end
+        return self.buf[start:end].view(dtype)
+
+    def gaps_intact(self):
+        return bool((self.buf.cpu().numpy()[~self.used] == CANARY).all())
+
+
+class Lists:
+    """A list of tensors of the given sizes beside its oracle."""
+
+    def __init__(self, sizes, grad="f32", param=None, bits8=False, seed=0, skew=1, sigma=1e-3, flat_offs=None, **hp):
+        torch = torch_mod()
+        from zero_partitioned_mixed_buffer_amd import binding as B
+        self.B, self.torch, self.sizes, self.kind, self.sigma = B, torch, sizes, grad, sigma
+        self.rng = np.random.default_rng(seed)
+        self.seed = int(self.rng.integers(2 ** 63)) * 2 + 1
+        self.rounding = hp.pop("rounding", "stochastic")
+        if not bits8:
+            self.rounding = "nearest"
+        self.clip = hp.pop("max_grad_norm", 0.0)
+        self.scaler = {k: hp.pop(k) for k in ("scale_interval", "scale_growth", "scale_backoff") if k in hp}
+        self.loss_scale = hp.pop("loss_scale", 1.0)
+        args = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01)
+        args.update(hp)
+        total = sum(sizes)
+        self.arena = Arena(total * 24 + len(sizes) * 480 + 4096)
+        take = self.arena.take
+        p0 = [(self.rng.standard_normal(n) * 0.02).astype(F32) for n in sizes]
+        self.p = [take(n, torch.float32, skew) for n in sizes]
+        for t, x in zip(self.p, p0):
+            t.copy_(torch.from_numpy(x))
+        gd = getattr(torch, GRADS[grad])
+        self.g = [take(n, gd, skew) for n in sizes]
+        self.w = [take(n, getattr(torch, GRADS[param]), skew) for n in sizes] if param else None
+        st = torch.float8_e4m3fn if bits8 else torch.float32
+        self.m = [take(n, st, skew) for n in sizes]
+        self.v = [take(n, st, skew) for n in sizes]
+        self.ms = self.vs = None
+        if bits8:
+            self.ms, self.vs = ([take(-(-n // 32), torch.float8_e8m0fnu, skew) for n in sizes] for _ in range(2))
+            for t in (*self.ms, *self.vs):
+                t.view(torch.uint8).fill_(1)
+        for t in (*self.m, *self.v, *(self.w or ())):
+            t.view(torch.uint8).zero_()
+        self.list = B.tensor_list(self.g, self.p, self.w, self.m, self.v, self.ms, self.vs, flat_offs)
+        self.ctl = torch.frombuffer(bytearray(B.ctl_init_bytes(self.loss_scale)), dtype=torch.uint8).cuda()
+        self.ws = torch.zeros(B.workspace_bytes(), dtype=torch.uint8, device="cuda")
+        self.ovf = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.sq = torch.zeros(1, dtype=torch.float64, device="cuda")
+        self.hp = B.adam_hp(*(args[k] for k in ("lr", "beta1", "beta2", "eps", "weight_decay")), self.clip,
+                            **self.scaler)
+        self.ref = to.TensorAdam(p0, 8 if bits8 else 32, **args, stochastic=self.rounding == "stochastic",
+                                 seed=self.seed, flat_offs=flat_offs)
+
+    def fill(self, scale, poison=None):
+        hosts = []
+        for i, (t, n) in enumerate(zip(self.g, self.sizes)):
+            x = (self.rng.standard_normal(n) * self.sigma * scale).astype(F32)
+            x[self.rng.random(n) < 0.1] = 0.0
+            if poison and poison[0] == i:
+                x[poison[1]] = poison[2]
+            d, h = as_grad(x, self.kind)
+            t.copy_(d)
+            hosts.append(h)
+        return hosts
+
+    def control(self):
+        return self.B.ctl_from_bytes(bytes(self.ctl.cpu().numpy().tobytes()))
+
+    def step(self, check=True, poison=None):
+        """One step on both sides; returns the control block."""
+        dyn = self.scaler.get("scale_interval", 0) > 0
+        scale = self.control()["loss_scale"] if dyn else self.loss_scale
+        hosts = self.fill(scale, poison)
+        B = self.B
+        if check:
+            B.tensors_grad_norm(self.list, self.ovf, self.sq, self.ws, scale, self.ctl if dyn else None)
+        B.tensors_adam_step(self.list, self.hp, self.ctl, self.ws, scale, self.ovf if check else None,
+                            self.sq if check else None, self.rounding, self.seed)
+        self.torch.cuda.synchronize()
+        ovf, sq = (int(self.ovf), float(self.sq)) if check else (0, 0.0)
+        if check:
+            want_ovf, want = to.grad_norm(hosts, scale)
+            assert ovf == int(want_ovf)
+            if not ovf:
+                assert abs(sq - want) <= 64 * 2.0 ** -53 * want
+        coef = min(1.0, self.clip / (np.sqrt(sq) + 1e-6)) if self.clip > 0 and not ovf else 1.0
+        if not ovf:
+            self.ref.step(hosts, scale, coef)
+        ctl = self.control()
+        assert (ctl["t"], ctl["overflow"], ctl["cur"]) == (self.ref.t, ovf, 0)
+        assert (ctl["beta1_pow"], ctl["beta2_pow"]) == (self.ref.b1p, self.ref.b2p)
+        if not ovf:
+            assert ctl["clip_coef"] == coef
+        if check and not ovf:
+            assert ctl["sumsq"] == sq
+        return ctl
+
+    def check(self, what=""):
+        torch = self.torch
+        for i, n in enumerate(self.sizes):
+            at = (what, i, n)
+            assert np.array_equal(bits(self.p[i]), self.ref.p[i].view(np.uint32)), ("master", at)
+            if self.w is not None:
+                want = torch.from_numpy(self.ref.p[i]).to(self.w[i].dtype)
+                assert torch.equal(self.w[i].cpu().view(torch.int16), want.view(torch.int16)), ("param", at)
+            for mine, scale, ref, name in ((self.m, self.ms, self.ref.m, "m"), (self.v, self.vs, self.ref.v, "v")):
+                if scale is None:
+                    assert np.array_equal(bits(mine[i]), ref[i].view(np.uint32)), (name, at)
+                else:
+                    assert np.array_equal(bits(scale[i]), ref[i][1]), (name + " scales", at)
+                    assert np.array_equal(bits(mine[i]), ref[i][0]), (name + " codes", at)
+        assert self.arena.gaps_intact(), what
+
+
+SIZES = [1, 2, 3, 0, 31, 32, 33, 1023, 1024, 1025, 4095, 4096, 4097, 5000, 12288, 20011]
+
+
+# --------------------------------------------------------------- 8-bit blocks
+def _values(n, root, seed):
+    """Values over many magnitudes, with blocks of zeros, of the smallest and
+    largest floats, and with an inf or a NaN among others."""
+    g = np.random.default_rng(seed)
+    x = g.standard_normal(n) * np.exp2(g.uniform(-12, 0, n)) * np.exp2(np.repeat(g.integers(-60, 60, n // 32 + 1), 32)[:n])
+    x = x.astype(F32)
+    if root:
+        x = np.abs(x)
+    if n >= 32 * 12:
+        b = x[:32 * 12].reshape(12, 32)
+        b[0] = 0.0
+        b[1] = np.exp2(g.uniform(-149, -126, 32)).astype(F32)
+        b[2] *= F32(0.0)
+        b[2, 5] = F32(2.0 ** -149)
+        b[3] = np.abs(g.standard_normal(32)).astype(F32) * F32(1e38)
+        b[4, 7] = np.inf
+        b[5, 31] = np.nan
+        b[6] = 448.0
+        b[6, 0] = 447.99997
+        b[7, 3] = 1e30
+        b[8] = F32(2.0 ** -9)
+        b[8, 1], b[8, 2] = 1.0, 2.0 ** -20
+        b[9, 0] = 0.0 if root else -0.0
+        b[10] = np.exp2(g.uniform(-140, -120, 32)).astype(F32)
+        if not root:
+            b[11, 4] = -np.inf
+    return x
+
+
+@pytest.mark.parametrize("root", [False, True])
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 64, 1000, 1024, 1025, 40003])
+def test_encode_decode(n, rounding, root):
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import mx8_decode, mx8_encode
+    x = _values(n, root, n)
+    seed, step, off = 0x123456789ABCDEF, 7, 2 ** 32 - 500
+    words = to.random_words(n, seed, step, off) if rounding == "stochastic" else None
+    codes, scales = to.mx8_encode(x, root, words)
+    for skew in (0, 1, 3):
+        a = Arena(n * 10 + 4096)
+        src, c, s = a.take(n, torch.float32, skew), a.take(n, torch.uint8, skew), a.take(-(-n // 32), torch.uint8, skew)
+        back = a.take(n, torch.float32, skew)
+        src.copy_(torch.from_numpy(x))
+        mx8_encode(src, c, s, root=root, rounding=rounding, seed=seed, step=step, flat_off=off)
+        mx8_decode(c, s, back, root=root)
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(s), scales), skew
+        bad = np.flatnonzero(bits(c) != codes)
+        assert bad.size == 0, (skew, bad[:5], x[bad[:5]], bits(c)[bad[:5]], codes[bad[:5]])
+        want = to.mx8_decode(codes, scales, root)
+        assert np.array_equal(back.cpu().numpy(), want, equal_nan=True)
+        assert a.gaps_intact() and np.array_equal(bits(src), x.view(np.uint32))
+
+
+def test_encode_negative_root_is_nan():
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import mx8_encode
+    x = torch.ones(64, device="cuda")
+    x[40] = -1.0
+    c, s = torch.zeros(64, dtype=torch.uint8, device="cuda"), torch.zeros(2, dtype=torch.uint8, device="cuda")
+    mx8_encode(x, c, s, root=True, rounding="nearest")
+    assert s.tolist()[1] == 255 and (c[32:] == 0x7F).all() and s.tolist()[0] != 255
+
+
+@pytest.mark.parametrize("root", [False, True])
+def test_decode_every_code_and_scale(root):
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import mx8_decode
+    codes = np.tile(np.arange(256, dtype=U8), 256)
+    scales = np.repeat(np.arange(256, dtype=U8), 8)
+    out = torch.empty(codes.size, device="cuda")
+    mx8_decode(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), out, root=root)
+    want = to.mx8_decode(codes, scales, root)
+    assert np.array_equal(out.cpu().numpy(), want, equal_nan=True)
+
+
+# ----------------------------------------------------------------------- norm
+@pytest.mark.parametrize("kind", list(GRADS))
+@pytest.mark.parametrize("sizes", [[1], [0], SIZES, [300001], [7] * 700])
+def test_norm(kind, sizes):
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import binding as B
+    g = np.random.default_rng(len(sizes))
+    a = Arena(sum(sizes) * 4 + 64 * len(sizes) + 4096)
+    dev, hosts = [], []
+    for n in sizes:
+        d, h = as_grad(g.standard_normal(n) * np.exp2(g.uniform(-14, 6, n)), kind)
+        t = a.take(n, d.dtype)
+        t.copy_(d)
+        dev.append(t)
+        hosts.append(h)
+    lst = B.tensor_list(dev)
+    ws = torch.zeros(B.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    ovf, sq = torch.full((1,), 9, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.float64, device="cuda")
+    for scale in (1.0, 1024.0, 3.7):
+        B.tensors_grad_norm(lst, ovf, sq, ws, scale)
+        _, want = to.grad_norm(hosts, scale)
+        assert int(ovf) == 0 and abs(float(sq) - want) <= 64 * 2.0 ** -53 * want
+    first = float(sq)
+    for _ in range(3):  # the same bits again
+        B.tensors_grad_norm(lst, ovf, sq, ws, 3.7)
+        assert float(sq) == first
+    for bad in (np.inf, -np.inf, np.nan):
+        where = [i for i, n in enumerate(sizes) if n]
+        for i in where[:1] + where[-1:]:
+            for j in {0, sizes[i] - 1}:
+                old = dev[i][j].clone()
+                dev[i][j] = bad
+                B.tensors_grad_norm(lst, ovf, sq, ws, 1.0)
+                assert int(ovf) == 1
+                dev[i][j] = old
+    B.tensors_grad_norm(lst, ovf, sq, ws, 3.7)
+    assert int(ovf) == 0 and float(sq) == first and a.gaps_intact()
+
+
+def test_norm_dynamic_scale_and_empty():
+    """L from the control block; a scale of 0 or one whose reciprocal
+    overflows flags even gradients of 0; an empty list gives 0."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import binding as B
+    ws = torch.zeros(B.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    ovf, sq = torch.full((1,), 9, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.float64, device="cuda")
+    empty = B.tensor_list([])
+    B.tensors_grad_norm(empty, ovf, sq, ws, 1.0)
+    assert int(ovf) == 0 and float(sq) == 0.0
+    g = torch.full((100,), 2.0, device="cuda")
+    zero = torch.zeros(100, device="cuda")
+    for scale, flag in ((8.0, 0), (0.0, 1), (1e-320, 1)):
+        ctl = torch.frombuffer(bytearray(B.ctl_init_bytes(scale)), dtype=torch.uint8).cuda()
+        for x in (g, zero):
+            B.tensors_grad_norm(B.tensor_list([x]), ovf, sq, ws, float("nan"), ctl)
+            assert int(ovf) == flag
+            if not flag:
+                assert float(sq) == (100 * 4.0 / 64 if x is g else 0.0)
+
+
+# ----------------------------------------------------------------------- adam
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("param", [None, "f16", "bf16"])
+@pytest.mark.parametrize("kind", list(GRADS))
+def test_steps_match_oracle(kind, param, bits8):
+    """Odd sizes at their elements' own alignment, four steps."""
+    x = Lists(SIZES, kind, param, bits8, seed=1, loss_scale=64.0)
+    for t in range(4):
+        x.step()
+        x.check(t)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("sizes", [[1], [32], [4096 * 3], [100003], [5] * 3000, [70001, 1, 262144, 33]])
+@pytest.mark.parametrize("skew", [0, 1])
+def test_steps_sizes(sizes, skew, bits8):
+    x = Lists(sizes, "bf16", "bf16", bits8, seed=2, skew=skew)
+    for t in range(2):
+        x.step(check=False)
+        x.check(t)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_clipped_steps(bits8):
+    x = Lists(SIZES, "f16", "f16", bits8, seed=3, max_grad_norm=0.05, loss_scale=256.0)
+    for t in range(3):
+        assert x.step()["clip_coef"] < 1.0
+        x.check(t)
+    x = Lists(SIZES, "f16", "f16", bits8, seed=3, max_grad_norm=1e3, loss_scale=256.0)
+    assert x.step()["clip_coef"] == 1.0
+    x.check()
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_nearest_and_other_hyperparameters(bits8):
+    x = Lists(SIZES, "f32", None, bits8, seed=4, rounding="nearest", beta1=0.0, beta2=0.5, eps=1e-3, lr=0.5,
+              weight_decay=0.0)
+    for t in range(3):
+        x.step(check=False)
+        x.check(t)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_overflow_skips_and_scale_moves(bits8):
+    """Steps 2 and 5 hold an inf or a NaN: nothing but the control block
+    changes, and the dynamic scale follows the scaler's rule."""
+    x = Lists(SIZES, "f16", "f16", bits8, seed=5, scale_interval=2, scale_growth=4.0, scale_backoff=0.5,
+              loss_scale=512.0)
+    scale, good, skipped = 512.0, 0, 0
+    for t, poison in enumerate([None, (0, 0, np.inf), None, None, (15, 20010, np.nan), None]):
+        ctl = x.step(poison=poison)
+        if poison:
+            scale, good, skipped = scale * 0.5, 0, skipped + 1
+        else:
+            good += 1
+            if good == 2:
+                scale, good = scale * 4.0, 0
+        assert (ctl["loss_scale"], ctl["good_steps"], ctl["skipped"]) == (scale, good, skipped)
+        x.check(t)
+
+
+def test_unchecked_inf_stays_in_its_block():
+    """Without a flag the step is taken: an inf reaches its own element, and
+    with 8-bit states the 32 of its block; everything else is as ever."""
+    for bits8 in (False, True):
+        x = Lists([100, 4097], "f32", "bf16", bits8, seed=6)
+        x.step(check=False)
+        x.step(check=False, poison=(1, 70, np.inf))
+        x.step(check=False)
+        for i in (0, 1):
+            p = x.p[i].cpu().numpy()
+            bad = np.flatnonzero(~np.isfinite(p))
+            lo, hi = (64, 96) if bits8 else (70, 71)
+            assert bad.tolist() == ([] if i == 0 else list(range(lo, hi)))
+            ok = np.isfinite(p)
+            assert np.array_equal(p[ok], x.ref.p[i][ok])
+        if bits8:
+            assert bits(x.ms[1])[2] == 255 and bits(x.vs[1])[2] == 255
+        assert x.arena.gaps_intact()
+
+
+def test_shared_gradient():
+    """One gradient tensor for two weights (a tied pair held twice)."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam
+    g = torch.randn(5000, device="cuda") * 1e-3
+    a = torch.randn(5000, device="cuda")
+    p, q = a.clone(), a.clone()
+    opt = TensorAdam([p, q], [g, g])
+    for _ in range(3):
+        opt.step()
+    assert torch.equal(p, q) and not torch.equal(p, a)
+    assert abs(float(opt.sumsq) - 2 * float(g.double().square().sum())) < 1e-12 * float(opt.sumsq)
+
+
+def test_same_as_the_fused_step():
+    """A one-slice window of fp16 gradients through zero_adam_step and the
+    same window as a list: the same weights, states and fp16 copies."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import OwnedShard, TensorAdam
+    n = 50003
+    g = np.random.default_rng(8)
+    p0 = torch.from_numpy((g.standard_normal(n) * 0.02).astype(F32)).cuda()
+    hp = dict(weight_decay=0.01, scale_interval=3, loss_scale=1024.0)
+    shard = OwnedShard(p0, **hp)
+    ag = torch.zeros(n, dtype=torch.float16, device="cuda")
+    shard.emit(ag)
+    cuts = [0, 7, 768, 30000, n]
+    flat, copy = p0.clone(), ag.clone()
+    slices = torch.zeros((1, (n + 7) // 8 * 8), dtype=torch.float16, device="cuda")
+    parts = lambda x: [x[a:b] for a, b in zip(cuts, cuts[1:])]  # noqa: E731
+    opt = TensorAdam(parts(flat), parts(slices[0]), parts(copy), **hp)
+    for t in range(7):
+        slices[0, :n] = torch.from_numpy((g.standard_normal(n) * 1e-3 * 1024).astype(F32)).half()
+        if t == 3:
+            slices[0, 777] = np.inf
+        shard.step(slices, allgather=ag)
+        opt.step()
+        torch.cuda.synchronize()
+        a, b = shard.control(), opt.control()
+        for k in ("t", "overflow", "good_steps", "beta1_pow", "beta2_pow", "skipped", "loss_scale"):
+            assert a[k] == b[k], (t, k)
+        p, m, v = shard.committed(a)
+        assert torch.equal(p, flat) and torch.equal(ag.view(torch.int16), copy.view(torch.int16))
+        for whole, mine in ((m, opt.exp_avg), (v, opt.exp_avg_sq)):
+            got = torch.cat([mine[o:o + k] for o, k in zip(opt.state_offs, opt.numels)])
+            assert torch.equal(whole, got)
+
+
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+def test_8_bit_step_is_decode_step_encode(rounding):
+    """The 8-bit step equals the 32-bit step between a decode and an encode
+    of the same arrays, bit for bit."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam, mx8_decode, mx8_encode
+    g = torch.Generator(device="cuda").manual_seed(4)
+    n = 9000
+    p8 = torch.randn(n, device="cuda", generator=g) * 0.02
+    p32, grad = p8.clone(), torch.empty(n, device="cuda", dtype=torch.bfloat16)
+    a = TensorAdam([p8], [grad], state_bits=8, rounding=rounding, seed=99, flat_offs=[12345])
+    b = TensorAdam([p32], [grad], state_bits=32)
+    for t in range(1, 5):
+        grad.copy_(torch.randn(n, device="cuda", generator=g) * 1e-3)
+        mx8_decode(a.exp_avg, a.avg_scale, b.exp_avg)
+        mx8_decode(a.exp_avg_sq, a.sq_scale, b.exp_avg_sq, root=True)
+        a.step()
+        b.step()
+        assert torch.equal(p8, p32)
+        for x, codes, scales, root in ((b.exp_avg, a.exp_avg, a.avg_scale, False),
+                                       (b.exp_avg_sq, a.exp_avg_sq, a.sq_scale, True)):
+            c, s = torch.zeros_like(codes.view(torch.uint8)), torch.ones_like(scales.view(torch.uint8))
+            mx8_encode(x[:n], c[:n], s[:-(-n // 32)], root=root, rounding=rounding, seed=99, step=t, flat_off=12345)
+            assert torch.equal(c, codes.view(torch.uint8)) and torch.equal(s, scales.view(torch.uint8)), (t, root)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_empty_list_still_counts_a_step(bits8):
+    x = Lists([0, 0], "f32", None, bits8, seed=7)
+    assert x.step()["t"] == 1
+    assert x.step(check=False)["t"] == 2
+
+
+# ------------------------------------------------------------ graphs, streams
+def _adam_pair(state_bits, n=70001, **kw):
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam
+    g = torch.Generator(device="cuda").manual_seed(3)
+    p0 = torch.randn(n, device="cuda", generator=g) * 0.02
+    out = []
+    for _ in range(2):
+        p, grad = p0.clone(), torch.zeros(n, device="cuda", dtype=torch.bfloat16)
+        w = p.to(torch.bfloat16)
+        cut = [0, 33, 5000, n]
+        parts = lambda x: [x[a:b] for a, b in zip(cut, cut[1:])]  # noqa: E731
+        out.append((TensorAdam(parts(p), parts(grad), parts(w), state_bits=state_bits, **kw), p, grad, w))
+    return out
+
+
+def _same(a, b):
+    torch = torch_mod()
+    (oa, pa, _, wa), (ob, pb, _, wb) = a, b
+    assert oa.control() == ob.control()
+    assert torch.equal(pa, pb) and torch.equal(wa, wb)
+    for k in ("exp_avg", "exp_avg_sq", "avg_scale", "sq_scale"):
+        x, y = getattr(oa, k), getattr(ob, k)
+        if x is not None:
+            assert np.array_equal(bits(x), bits(y)), k
+
+
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_graph_replays_match_eager_steps(state_bits):
+    """Two steps captured and replayed with fresh gradients: the step number,
+    the random words and the dynamic scale all move on the device."""
+    torch = torch_mod()
+    eager, graphed = _adam_pair(state_bits, max_grad_norm=0.1, scale_interval=3, loss_scale=8.0, seed=5)
+    for o in (eager, graphed):
+        o[0].step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed[0].step()
+        graphed[0].step()
+    for rep in range(4):
+        x = (torch.randn(eager[2].shape, device="cuda") * 8e-3).bfloat16()
+        if rep == 2:
+            x[123] = float("inf")
+        eager[2].copy_(x)
+        graphed[2].copy_(x)
+        torch.cuda.synchronize()
+        graph.replay()
+        eager[0].step()
+        eager[0].step()
+        torch.cuda.synchronize()
+        _same(eager, graphed)
+    assert eager[0].control()["skipped"] == 2
+
+
+def test_two_streams():
+    """Two lists stepped at once on two streams, each with its own workspace."""
+    torch = torch_mod()
+    pairs = [_adam_pair(8, n=3000001, seed=1), _adam_pair(32, n=2500007)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for t in range(6):
+        for (alone, other), s in zip(pairs, streams):
+            with torch.cuda.stream(s):
+                x = (torch.randn(other[2].shape, device="cuda") * 1e-3).bfloat16()
+                other[2].copy_(x)
+                alone[2].copy_(x)
+                other[0].step()
+    torch.cuda.synchronize()
+    for (alone, other), s in zip(pairs, streams):
+        assert other[0].control()["t"] == 6
+    # the same gradients one after another give the same as two at once
+    torch.manual_seed(11)
+    grads = [[(torch.randn(p[1][2].shape, device="cuda") * 1e-3).bfloat16() for _ in range(4)] for p in pairs]
+    pairs = [_adam_pair(8, n=3000001, seed=1), _adam_pair(32, n=2500007)]
+    torch.cuda.synchronize()
+    for t in range(4):
+        for (alone, other), s, g in zip(pairs, streams, grads):
+            with torch.cuda.stream(s):
+                other[2].copy_(g[t])
+                other[0].step()
+    torch.cuda.synchronize()
+    for (alone, other), g in zip(pairs, grads):
+        for t in range(4):
+            alone[2].copy_(g[t])
+            alone[0].step()
+        torch.cuda.synchronize()
+        _same(alone, other)
+
+
+def test_other_gradients_and_refusals():
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam, binding as B
+    (a, pa, ga, wa), (b, pb, gb, wb) = _adam_pair(8)
+    x = (torch.randn(ga.shape, device="cuda") * 1e-3).bfloat16()
+    ga.copy_(x)
+    a.step()
+    cut = [0, 33, 5000, gb.numel()]
+    b.set_grads([x[i:j].clone() for i, j in zip(cut, cut[1:])])
+    b.step()
+    torch.cuda.synchronize()
+    assert torch.equal(pa, pb) and torch.equal(wa, wb)
+    with pytest.raises(ValueError, match="expected"):
+        b.set_grads([x[:10], x[:10], x[:10]])
+    assert len(b.grads) == 3 and b.grads[0].numel() == 33
+    with pytest.raises(B.ZeroError):
+        TensorAdam([pa, pa], [x, x])  # the same weight twice
+    with pytest.raises(B.ZeroError):
+        TensorAdam([pa[:100], pa[99:200]], [x[:100], x[99:200]])
+
+
+# ----------------------------------------------------------------- checkpoint
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_checkpoint_resumes_exactly(state_bits, tmp_path):
+    torch = torch_mod()
+    whole, resumed = _adam_pair(state_bits, seed=77, scale_interval=2, loss_scale=4.0)
+    grads = [(torch.randn(whole[2].shape, device="cuda") * 4e-3).bfloat16() for _ in range(6)]
+    for t in range(3):
+        whole[2].copy_(grads[t])
+        whole[0].step()
+    whole[0].save(str(tmp_path / "s.npz"))
+    resumed[0].load(str(tmp_path / "s.npz"))
+    _same(whole, resumed)
+    for t in range(3, 6):
+        for o in (whole, resumed):
+            o[2].copy_(grads[t])
+            o[0].step()
+    torch.cuda.synchronize()
+    _same(whole, resumed)
+
+
+def test_checkpoint_between_widths():
+    """A 32-bit state into an 8-bit list and back: what the oracle encodes to
+    nearest and decodes."""
+    torch = torch_mod()
+    a, b = _adam_pair(32)[0], _adam_pair(8)[0]
+    for t in range(3):
+        a[2].copy_((torch.randn(a[2].shape, device="cuda") * 1e-3).bfloat16())
+        a[0].step()
+    b[0].load_state_dict(a[0].state_dict())
+    assert torch.equal(a[1], b[1]) and torch.equal(a[3], b[3]) and a[0].control() == b[0].control()
+    back = _adam_pair(32)[0]
+    back[0].load_state_dict(b[0].state_dict())
+    for k, s, root in (("exp_avg", "avg_scale", False), ("exp_avg_sq", "sq_scale", True)):
+        x = getattr(a[0], k).cpu().numpy()
+        codes, scales = to.mx8_encode(x, root)
+        assert np.array_equal(bits(getattr(b[0], k)), codes) and np.array_equal(bits(getattr(b[0], s)), scales)
+        assert np.array_equal(getattr(back[0], k).cpu().numpy(), to.mx8_decode(codes, scales, root))
+    with pytest.raises(ValueError, match="sizes"):
+        back[0].load_state_dict({**a[0].state_dict(), "numels": np.array([1, 2, 3])})
+
+
+# -------------------------------------------------------------- long tensors
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_past_the_int32_range(state_bits):
+    """One tensor of 2^31 + 4163 elements: the elements around 2^31 and at the
+    end step as the same elements in a short list with the same counters (spans of
+    whole
+    blocks, but for the last: a block cut short would have its own scale)."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam
+    n = 2 ** 31 + 4163
+    g = torch.Generator(device="cuda").manual_seed(1)
+    p = torch.empty(n, device="cuda")
+    grad = torch.empty(n, device="cuda", dtype=torch.bfloat16)
+    for lo in range(0, n, 1 << 28):
+        k = min(1 << 28, n - lo)
+        p[lo:lo + k].normal_(0, 0.02, generator=g)
+        grad[lo:lo + k].normal_(0, 1e-3, generator=g)
+    spans = [(0, 5024), (2 ** 31 - 4096, 2 ** 31 + 4096), (n - 4163 - 32, n)]
+    small_p = [p[a:b].clone() for a, b in spans]
+    small_g = [grad[a:b].clone() for a, b in spans]
+    off = 2 ** 40 + 3
+    whole = TensorAdam([p], [grad], state_bits=state_bits, seed=3, flat_offs=[off], check_finite=False)
+    few = TensorAdam(small_p, small_g, state_bits=state_bits, seed=3, flat_offs=[off + a for a, _ in spans],
+                     check_finite=False)
+    for _ in range(2):
+        whole.step()
+        few.step()
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(spans):
+        assert torch.equal(p[a:b], small_p[i]), (a, b)
+        o = few.state_offs[i]
+        for k in ("exp_avg", "exp_avg_sq"):
+            assert np.array_equal(bits(getattr(whole, k)[a:b]), bits(getattr(few, k)[o:o + b - a])), (k, a)
+    ws = whole.workspace
+    from zero_partitioned_mixed_buffer_amd import binding as B
+    B.tensors_grad_norm(whole.list, whole.overflow, whole.sumsq, ws)
+    want = sum(float(x.double().square().sum()) for x in grad.split(1 << 26))
+    # a lane of this grid adds up to 2^31 / (2^11 * 2^8) * 2 = 2^13 terms before the trees
+    assert abs(float(whole.sumsq) - want) <= (2 ** 13 + 64) * 2.0 ** -53 * want

@@ -31,6 +31,7 @@ EXPORTED = (
     "zero_adam_step", "zero_adam_step_clipped", "zero_adam_step_bucket", "zero_restore_skipped",
     "zero_emit_fp16", "zero_gather_params", "zero_adam_step_noalloc", "zero_calib_triad",
     "zero_calib_stream_mix", "zero_adam_step_buckets", "zero_gather_layers", "zero_calib_slice_read",
+    "zero_tensors_plan", "zero_tensors_grad_norm", "zero_tensors_adam_step", "zero_mx8_encode", "zero_mx8_decode",
 )
 ABI_VERSION = 7
 BUCKET_FIRST = 1
@@ -77,6 +78,20 @@ class Bucket(C.Structure):
 
 
 MAX_BUCKETS_PER_CALL = 1024
+MX8_BLOCK = 32
+TYPE_NONE, TYPE_F32, TYPE_F16, TYPE_BF16, TYPE_MX8 = range(5)
+ROUNDING = {"nearest": 0, "stochastic": 1}
+
+
+class Tensor(C.Structure):
+    _fields_ = [(k, C.c_void_p) for k in ("master", "grad", "param", "exp_avg", "exp_avg_sq", "avg_scale",
+                                          "sq_scale")] + \
+               [("n", C.c_int64), ("flat_off", C.c_int64), ("reserved", C.c_int64)]
+
+
+class TensorListInfo(C.Structure):
+    _fields_ = [(k, C.c_int32) for k in ("n_tensors", "grad_type", "param_type", "state_type")] + \
+               [(k, C.c_int64) for k in ("n_elems", "n_chunks", "table_bytes", "reserved")]
 
 
 class AdamState(C.Structure):
@@ -137,7 +152,15 @@ def lib():
     L.zero_calib_triad.argtypes = [P, P, P, C.c_float, C.c_int64, P]
     L.zero_calib_stream_mix.argtypes = [C.POINTER(GradSrc), C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), P, P]
     L.zero_calib_slice_read.argtypes = [C.POINTER(GradSrc), P, P]
-    for name in ("zero_plan_partitions", "zero_memory_model", "zero_reduce_owned", "zero_adam_step",
+    L.zero_tensors_plan.argtypes = [C.POINTER(Tensor), C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                                    C.POINTER(TensorListInfo), P, C.c_int64]
+    L.zero_tensors_grad_norm.argtypes = [C.POINTER(TensorListInfo), P, C.c_double, P, P, P, P, P]
+    L.zero_tensors_adam_step.argtypes = [C.POINTER(TensorListInfo), P, C.POINTER(AdamHp), C.c_double, P, P, P,
+                                         C.c_int32, C.c_uint64, P, P]
+    L.zero_mx8_encode.argtypes = [P, C.c_int64, C.c_int32, P, P, C.c_int32, C.c_uint64, C.c_int64, C.c_int64, P]
+    L.zero_mx8_decode.argtypes = [P, P, C.c_int64, C.c_int32, P, P]
+    for name in ("zero_tensors_plan", "zero_tensors_grad_norm", "zero_tensors_adam_step", "zero_mx8_encode",
+                 "zero_mx8_decode", "zero_plan_partitions", "zero_memory_model", "zero_reduce_owned", "zero_adam_step",
                  "zero_adam_step_noalloc", "zero_calib_triad", "zero_calib_stream_mix", "zero_adam_step_buckets",
                  "zero_gather_layers", "zero_calib_slice_read",
                  "zero_adam_step_clipped", "zero_adam_step_bucket", "zero_restore_skipped", "zero_emit_fp16",
@@ -427,6 +450,189 @@ def gather_layers(windows: Sequence, part: int, ranges: Sequence[Tuple[int, int]
     dst = (C.c_void_p * max(len(dsts), 1))(*[_ptr(d) for d in dsts])
     _check(lib().zero_gather_layers(arr, len(windows), int(part), rng, len(ranges), dst, _stream(stream)),
            "zero_gather_layers")
+
+
+# ----------------------------------------------------------------- tensor lists
+_LIST_TYPES = {"float32": TYPE_F32, "float16": TYPE_F16, "bfloat16": TYPE_BF16}
+_CODES = ("float8_e4m3fn", "uint8")
+_SCALES = ("float8_e8m0fnu", "uint8")
+
+
+def _check_current(t, what: str):
+    """A tensor of the current device: the launch goes to that device's stream."""
+    if _is_tensor(t):
+        import torch
+        if not t.is_cuda:
+            raise ValueError(f"{what}: must be a device tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{what}: on {t.device}, but the current device is {torch.cuda.current_device()}")
+
+
+def _common_dtype(tensors: Sequence, kinds: Tuple[str, ...], what: str) -> str:
+    names = {_dtype_name(t) for t in tensors}
+    if len(names) > 1 or not names <= set(kinds):
+        raise ValueError(f"{what}: one dtype of {kinds} expected, got {sorted(names)}")
+    return names.pop() if names else kinds[0]
+
+
+class TensorList:
+    """A planned list of tensors: its table in device memory, and the tensors
+    it points to (kept alive here).  Made by tensor_list()."""
+
+    def __init__(self, info: TensorListInfo, table, tensors):
+        self.info = info
+        self.table = table
+        self.tensors = tensors
+        self.numel = int(info.n_elems)
+
+
+def tensor_list(grads: Sequence, masters: Optional[Sequence] = None, params: Optional[Sequence] = None,
+                exp_avg: Optional[Sequence] = None, exp_avg_sq: Optional[Sequence] = None,
+                avg_scale: Optional[Sequence] = None, sq_scale: Optional[Sequence] = None,
+                flat_offs: Optional[Sequence[int]] = None) -> TensorList:
+    """Plans a list of torch tensors on the current device (zero_tensors_plan)
+    and uploads its table.
+
+    ``grads`` alone makes a list for norms.  A list for steps has as many
+    ``masters`` (float32), ``exp_avg`` and ``exp_avg_sq`` (float32; or e4m3
+    codes, and then ``avg_scale`` and ``sq_scale`` with one byte for 32
+    elements), and may have 16-bit ``params``.  Every tensor is contiguous,
+    and the list holds their addresses: plan again when one moves.
+    ``flat_offs`` are the tensors' first random counters (default: packed in
+    list order)."""
+    import torch
+    count = len(grads)
+    given = {"masters": masters, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq}
+    steps = masters is not None
+    if any((v is not None) != steps for v in given.values()):
+        raise ValueError("masters, exp_avg and exp_avg_sq come together")
+    if not steps and (params is not None or avg_scale is not None or sq_scale is not None):
+        raise ValueError("a list of gradients alone has no params and no scales")
+    columns = {"grads": grads, "masters": masters, "params": params, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
+               "avg_scale": avg_scale, "sq_scale": sq_scale, "flat_offs": flat_offs}
+    for what, col in columns.items():
+        if col is not None and len(col) != count:
+            raise ValueError(f"{what}: {len(col)} entries for {count} gradients")
+    gtype = _LIST_TYPES[_common_dtype(grads, tuple(_LIST_TYPES), "gradients")]
+    ptype, stype = TYPE_NONE, TYPE_NONE
+    numels = [int(g.numel()) for g in grads]
+    if steps:
+        _common_dtype(masters, ("float32",), "master weights")
+        if params is not None:
+            ptype = _LIST_TYPES[_common_dtype(params, ("float16", "bfloat16"), "params")]
+        kind = _common_dtype([*exp_avg, *exp_avg_sq], ("float32", *_CODES), "states")
+        stype = TYPE_F32 if kind == "float32" else TYPE_MX8
+        if (stype == TYPE_MX8) != (avg_scale is not None) or (stype == TYPE_MX8) != (sq_scale is not None):
+            raise ValueError("states in 8 bits, and no others, come with avg_scale and sq_scale")
+        if stype == TYPE_MX8:
+            _common_dtype([*avg_scale, *sq_scale], _SCALES, "scales")
+    keep = []
+    for what, col in columns.items():
+        if col is None or what == "flat_offs":
+            continue
+        for t, n in zip(col, numels):
+            want = -(-n // MX8_BLOCK) if what.endswith("scale") else n
+            if t.numel() != want:
+                raise ValueError(f"{what}: {t.numel()} elements where {want} are expected")
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: tensors must be contiguous")
+        keep.append(list(col))
+    for col in keep:
+        for t in col:
+            _check_current(t, "tensor list")
+    if flat_offs is None:
+        flat_offs = [0] * count
+        for i in range(1, count):
+            flat_offs[i] = flat_offs[i - 1] + numels[i - 1]
+    arr = (Tensor * max(count, 1))()
+    for i in range(count):
+        t = arr[i]
+        t.n, t.flat_off, t.grad = numels[i], int(flat_offs[i]), _ptr(grads[i])
+        if steps:
+            t.master, t.exp_avg, t.exp_avg_sq = _ptr(masters[i]), _ptr(exp_avg[i]), _ptr(exp_avg_sq[i])
+            if params is not None:
+                t.param = _ptr(params[i])
+            if stype == TYPE_MX8:
+                t.avg_scale, t.sq_scale = _ptr(avg_scale[i]), _ptr(sq_scale[i])
+    info = TensorListInfo()
+    st = lib().zero_tensors_plan(arr, count, gtype, ptype, stype, C.byref(info), None, 0)
+    if st not in (ZERO_OK, ZERO_ECAPACITY):
+        _check(st, "zero_tensors_plan")
+    if info.table_bytes == 0:
+        return TensorList(info, None, keep)
+    host = torch.empty(int(info.table_bytes) + 16, dtype=torch.uint8)
+    host = host[-host.data_ptr() % 16:][:int(info.table_bytes)]
+    _check(lib().zero_tensors_plan(arr, count, gtype, ptype, stype, C.byref(info), host.data_ptr(), host.numel()),
+           "zero_tensors_plan")
+    return TensorList(info, host.to(torch.device("cuda", torch.cuda.current_device())), keep)
+
+
+def tensors_grad_norm(lst: TensorList, overflow, sumsq, workspace, loss_scale: float = 1.0, ctl=None, stream=None):
+    """sum g^2 of the list's gradients over ``loss_scale`` (or the control
+    block's scale) into ``sumsq``, and whether it is not finite into ``overflow``."""
+    for t, kind, what in ((overflow, "int32", "overflow flag"), (sumsq, "float64", "sum of squares")):
+        _check_span(t, 0, 1, (kind,), what)
+        _check_current(t, what)
+    _check_ws(workspace)
+    _check_ctl(ctl)
+    _check_current(lst.table, "tensor list")
+    _check(lib().zero_tensors_grad_norm(C.byref(lst.info), _ptr(lst.table), float(loss_scale), _ptr(ctl),
+                                        _ptr(overflow), _ptr(sumsq), _ptr(workspace), _stream(stream)),
+           "zero_tensors_grad_norm")
+
+
+def _check_ctl(ctl):
+    if _is_tensor(ctl) and (ctl.numel() * ctl.element_size() < CTL_BYTES or not ctl.is_cuda):
+        raise ValueError(f"control block: a device tensor of at least {CTL_BYTES} bytes")
+
+
+def _rounding(name: str) -> int:
+    if name not in ROUNDING:
+        raise ValueError(f"rounding: {name!r}, expected one of {tuple(ROUNDING)}")
+    return ROUNDING[name]
+
+
+def tensors_adam_step(lst: TensorList, hp: AdamHp, ctl, workspace, loss_scale: float = 1.0, overflow=None,
+                      sumsq=None, rounding: str = "nearest", seed: int = 0, stream=None):
+    """One Adam/AdamW step of every tensor of the list, in place."""
+    if overflow is not None:
+        _check_span(overflow, 0, 1, ("int32",), "overflow flag")
+    if sumsq is not None:
+        _check_span(sumsq, 0, 1, ("float64",), "sum of squares")
+    _check_ws(workspace)
+    _check_ctl(ctl)
+    for t, what in ((overflow, "overflow flag"), (sumsq, "sum of squares"), (ctl, "control block"),
+                    (lst.table, "tensor list")):
+        _check_current(t, what)
+    _check(lib().zero_tensors_adam_step(C.byref(lst.info), _ptr(lst.table), C.byref(hp), float(loss_scale),
+                                        _ptr(ctl), _ptr(overflow), _ptr(sumsq), _rounding(rounding),
+                                        int(seed) & (2**64 - 1), _ptr(workspace), _stream(stream)),
+           "zero_tensors_adam_step")
+
+
+def _check_mx8(x, codes, scales):
+    n = int(x.numel())
+    for t, off, kinds, what in ((x, n, ("float32",), "array"), (codes, n, _CODES, "codes"),
+                                (scales, -(-n // MX8_BLOCK), _SCALES, "scales")):
+        _check_span(t, 0, off, kinds, what)
+        _check_current(t, what)
+    return n
+
+
+def mx8_encode(x, codes, scales, root: bool = False, rounding: str = "stochastic", seed: int = 0, step: int = 0,
+               flat_off: int = 0, stream=None):
+    """A float32 tensor into 8-bit blocks: its values, or their square roots."""
+    n = _check_mx8(x, codes, scales)
+    _check(lib().zero_mx8_encode(_ptr(x), n, int(bool(root)), _ptr(codes), _ptr(scales), _rounding(rounding),
+                                 int(seed) & (2**64 - 1), int(step), int(flat_off), _stream(stream)),
+           "zero_mx8_encode")
+
+
+def mx8_decode(codes, scales, x, root: bool = False, stream=None):
+    """8-bit blocks into a float32 tensor: the values, or their squares."""
+    n = _check_mx8(x, codes, scales)
+    _check(lib().zero_mx8_decode(_ptr(codes), _ptr(scales), n, int(bool(root)), _ptr(x), _stream(stream)),
+           "zero_mx8_decode")
 
 
 # ------------------------------------------------------------------ calibration

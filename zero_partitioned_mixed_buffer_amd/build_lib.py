@@ -3,8 +3,8 @@
     python -m zero_partitioned_mixed_buffer_amd.build_lib [--asm]
 
 The host translation units (planner, memory model, argument validation and
-the C entry points) are compiled with g++, the HIP translation unit
-(kernels and their launchers) with hipcc, and both are linked into one
+the C entry points) are compiled with g++, the HIP translation units
+(kernels and their launchers) with hipcc, and all are linked into one
 shared library next to this file.  ``--asm`` also writes the gfx950
 assembly of the kernels to _build/ for inspection.  (hostcheck_build.py
 builds the host units alone under the sanitizers.)
@@ -22,9 +22,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libzero_dp.so")
-HOST_SOURCES = ("zero_dp_host.cpp", "zero_dp_calls.cpp")
-# the step's kernels and launchers; the benchmark's calibration kernels
-DEVICE_SOURCES = ("zero_dp_kernels.hip", "zero_dp_calib.hip")
+HOST_SOURCES = ("zero_dp_host.cpp", "zero_dp_calls.cpp", "zero_dp_tensors.cpp")
+# the step's kernels and launchers; the tensor-list operators'; the
+# benchmark's calibration kernels
+DEVICE_SOURCES = ("zero_dp_kernels.hip", "zero_dp_tensors.hip", "zero_dp_calib.hip")
 ARCH = "gfx950"
 
 HIP_FLAGS = [
@@ -64,13 +65,13 @@ def build(verbose: bool = False, asm: bool = False) -> str:
         objs.append(o)
     dev_objs = []
     for src in DEVICE_SOURCES:
-        o = os.path.join(BUILD, src.replace(".hip", ".o"))
+        o = os.path.join(BUILD, src.replace(".hip", "_hip.o"))
         _run([hipcc, *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", o], verbose)
         dev_objs.append(o)
     if asm:
-        _run([hipcc, *HIP_FLAGS, "-I", INCLUDE, "--cuda-device-only", "-S",
-              os.path.join(CSRC, "zero_dp_kernels.hip"), "-o", os.path.join(BUILD, "zero_dp_kernels.s")],
-             verbose)
+        for src in DEVICE_SOURCES[:2]:
+            _run([hipcc, *HIP_FLAGS, "-I", INCLUDE, "--cuda-device-only", "-S", os.path.join(CSRC, src), "-o",
+                  os.path.join(BUILD, src.replace(".hip", ".s"))], verbose)
     tmp = LIB + ".tmp"
     _run([hipcc, "-shared", f"--offload-arch={ARCH}", "-fPIC", *objs, *dev_objs, "-o", tmp,
           "-Wl,-rpath,/opt/rocm/lib"], verbose)

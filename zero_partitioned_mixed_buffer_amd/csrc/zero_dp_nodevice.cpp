@@ -6,6 +6,7 @@
 // nothing here computes anything.
 #include "zero_dp_calib.h"
 #include "zero_dp_internal.h"
+#include "zero_dp_tensors.h"
 
 namespace {
 
@@ -42,5 +43,13 @@ int scratch_workspace(void**) { return no_device(); }
 int launch_calib_triad(float*, const float*, const float*, float, int64_t, void*) { return no_device(); }
 int launch_calib_mix(const SrcArgs&, const float* const*, float* const*, uint16_t*, void*) { return no_device(); }
 int launch_calib_slice_read(const SrcArgs&, uint32_t*, void*) { return no_device(); }
+int launch_tensors_norm(const ListArgs&, double, const zero_step_ctl*, int32_t*, double*, const Partials&, void*) {
+    return no_device();
+}
+int launch_tensors_adam(const ListArgs&, const TensorStepArgs&, void*) { return no_device(); }
+int launch_mx8_encode(const float*, int64_t, bool, uint8_t*, uint8_t*, bool, uint64_t, uint32_t, uint64_t, void*) {
+    return no_device();
+}
+int launch_mx8_decode(const uint8_t*, const uint8_t*, int64_t, bool, float*, void*) { return no_device(); }
 
 }  // namespace zdp

@@ -1,0 +1,215 @@
+"""Adam/AdamW over a list of tensors, with states in 32 or in 8 bits.
+
+Holds the list's states, control block and workspace (allocated with torch)
+and forwards each step to the library: zero_tensors_grad_norm where the
+gradients are checked or clipped, then zero_tensors_adam_step.  Nothing here
+synchronises with the device but control() and the checkpoint calls.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional, Sequence
+
+from . import binding as B
+
+_ALIGN = 64  # elements between the starts a state may have in its buffer
+
+
+class TensorAdam:
+    """``masters``: float32 tensors, stepped in place.  ``grads``: their
+    gradients, all float32, float16 or bfloat16.  ``params``: float16 or
+    bfloat16 copies of the weights that each step writes, or None.
+
+    The states lie in one buffer each (``exp_avg``, ``exp_avg_sq``; with
+    state_bits=8 also ``avg_scale`` and ``sq_scale``), tensor i from element
+    state_offs[i], a multiple of 64, with zeros in the gaps.  With 8 bits
+    ``exp_avg_sq`` holds the variance's root.  Fill them in place.
+
+    check_finite (default) takes a pass over the gradients first and skips
+    the step if any is inf or NaN; max_grad_norm > 0 (clipping) and
+    scale_interval > 0 (dynamic loss scaling, from ``loss_scale``) need it.
+    """
+
+    def __init__(self, masters: Sequence, grads: Sequence, params: Optional[Sequence] = None,
+                 flat_offs: Optional[Sequence[int]] = None, state_bits: int = 32, lr=1e-3, beta1=0.9, beta2=0.999,
+                 eps=1e-8, weight_decay=0.0, max_grad_norm=0.0, check_finite=True, scale_interval=0,
+                 scale_growth=2.0, scale_backoff=0.5, loss_scale=1.0, rounding="stochastic", seed=0):
+        import torch
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits: {state_bits}, expected 8 or 32")
+        if not masters:
+            raise ValueError("an empty list of tensors")
+        if not check_finite and (max_grad_norm > 0 or scale_interval > 0):
+            raise ValueError("clipping and dynamic loss scaling need check_finite")
+        B._rounding(rounding)
+        self.device = masters[0].device
+        if self.device.type != "cuda":
+            raise ValueError("masters: must be device tensors")
+        self.masters, self.grads = list(masters), list(grads)
+        self.params = list(params) if params is not None else None
+        self.flat_offs = None if flat_offs is None else [int(x) for x in flat_offs]
+        self.state_bits = state_bits
+        self.numels = [int(t.numel()) for t in self.masters]
+        self.state_offs, total = [], 0
+        for n in self.numels:
+            self.state_offs.append(total)
+            total += -(-n // _ALIGN) * _ALIGN
+        dev = self.device
+        with torch.cuda.device(dev):
+            if state_bits == 8:
+                def byte(n, x, kind):
+                    return torch.full((n,), x, dtype=torch.uint8, device=dev).view(kind)
+                self.exp_avg, self.exp_avg_sq = (byte(total, 0, torch.float8_e4m3fn) for _ in range(2))
+                # the scale byte of an encoded block of zeros
+                self.avg_scale, self.sq_scale = (byte(total // B.MX8_BLOCK, 1, torch.float8_e8m0fnu)
+                                                 for _ in range(2))
+            else:
+                self.exp_avg, self.exp_avg_sq = (torch.zeros(total, dtype=torch.float32, device=dev)
+                                                 for _ in range(2))
+                self.avg_scale = self.sq_scale = None
+            self.ctl = torch.frombuffer(bytearray(B.ctl_init_bytes(loss_scale)), dtype=torch.uint8).to(dev)
+            self.workspace = torch.zeros(B.workspace_bytes(), dtype=torch.uint8, device=dev)
+            self.overflow = torch.zeros(1, dtype=torch.int32, device=dev)
+            self.sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
+        self.hp = B.adam_hp(lr, beta1, beta2, eps, weight_decay, max_grad_norm, scale_interval, scale_growth,
+                            scale_backoff)
+        self.loss_scale = float(loss_scale)
+        self.check_finite = bool(check_finite)
+        self.rounding = rounding if state_bits == 8 else "nearest"
+        self.seed = int(seed)
+        self._plan()
+
+    def _views(self, flat, per=1):
+        return [flat[o // per:o // per + -(-n // per)] for o, n in zip(self.state_offs, self.numels)]
+
+    def _plan(self):
+        import torch
+        mx = self.state_bits == 8
+        with torch.cuda.device(self.device):
+            self.list = B.tensor_list(self.grads, self.masters, self.params, self._views(self.exp_avg),
+                                      self._views(self.exp_avg_sq),
+                                      self._views(self.avg_scale, B.MX8_BLOCK) if mx else None,
+                                      self._views(self.sq_scale, B.MX8_BLOCK) if mx else None, self.flat_offs)
+
+    def set_grads(self, grads: Sequence):
+        """Other gradient tensors of the same sizes, from the next step on."""
+        old, self.grads = self.grads, list(grads)
+        try:
+            self._plan()
+        except Exception:
+            self.grads = old
+            raise
+
+    def step(self, stream=None):
+        """One step on what the gradient tensors hold, scaled by ``loss_scale``
+        (with dynamic scaling by the control block's)."""
+        import torch
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.step(stream)
+        s = B._stream(stream)
+        L, info, table = B.lib(), C.byref(self.list.info), self.list.table
+        table = None if table is None else table.data_ptr()
+        ctl, ws = self.ctl.data_ptr(), self.workspace.data_ptr()
+        overflow = sumsq = None
+        if self.check_finite:
+            overflow, sumsq = self.overflow.data_ptr(), self.sumsq.data_ptr()
+            dyn = ctl if self.hp.scale_interval > 0 else None
+            B._check(L.zero_tensors_grad_norm(info, table, self.loss_scale, dyn, overflow, sumsq, ws, s),
+                     "zero_tensors_grad_norm")
+        B._check(L.zero_tensors_adam_step(info, table, C.byref(self.hp), self.loss_scale, ctl, overflow, sumsq,
+                                          B.ROUNDING[self.rounding], self.seed & (2**64 - 1), ws, s),
+                 "zero_tensors_adam_step")
+
+    def control(self) -> dict:
+        """Reads the device control block (synchronises with the device)."""
+        return B.ctl_from_bytes(bytes(self.ctl.cpu().numpy().tobytes()))
+
+    def set_step(self, t: int):
+        """Makes ``t`` the number of steps taken so far (beta powers as t
+        successive products)."""
+        if t < 0:
+            raise ValueError("a negative step count")
+        c = self.control()
+        c["t"], c["beta1_pow"], c["beta2_pow"] = int(t), 1.0, 1.0
+        for _ in range(int(t)):
+            c["beta1_pow"] *= self.hp.beta1
+            c["beta2_pow"] *= self.hp.beta2
+        self._write_control(c)
+
+    def _write_control(self, fields: dict):
+        import torch
+        self.ctl.copy_(torch.frombuffer(bytearray(B.ctl_to_bytes(fields)), dtype=torch.uint8))
+
+    # ------------------------------------------------------------ checkpoint
+    def state_dict(self) -> dict:
+        """Host copies of the weights, states (codes and scale bytes as uint8
+        for 8 bits) and the control block.  Synchronises with the device."""
+        import numpy as np
+        import torch
+
+        def host(x):
+            return (x if x.dtype == torch.float32 else x.view(torch.uint8)).cpu().numpy()
+
+        out = {"numels": np.asarray(self.numels, dtype=np.int64),
+               "master": np.concatenate([m.detach().reshape(-1).cpu().numpy() for m in self.masters]),
+               "exp_avg": host(self.exp_avg), "exp_avg_sq": host(self.exp_avg_sq),
+               "ctl": np.frombuffer(self.ctl.cpu().numpy().tobytes(), dtype=np.uint8).copy()}
+        if self.state_bits == 8:
+            out["avg_scale"], out["sq_scale"] = host(self.avg_scale), host(self.sq_scale)
+        return out
+
+    def load_state_dict(self, sd: dict):
+        """Restores a state_dict of a list of the same sizes.  Of the same
+        state_bits it resumes exactly; states of the other width are encoded
+        (to nearest) or decoded.  The 16-bit copies are written anew."""
+        import numpy as np
+        import torch
+        if [int(x) for x in np.asarray(sd["numels"])] != self.numels:
+            raise ValueError("numels: the state_dict is of a list of other sizes")
+        raw = np.asarray(sd["ctl"], dtype=np.uint8).tobytes()
+        if len(raw) != B.CTL_BYTES:
+            raise ValueError(f"control block: expected {B.CTL_BYTES} bytes, got {len(raw)}")
+        total = self.exp_avg.numel()
+        mx = "avg_scale" in sd
+        want = {"master": (np.float32, sum(self.numels))}
+        for k in ("exp_avg", "exp_avg_sq"):
+            want[k] = (np.uint8 if mx else np.float32, total)
+        if mx:
+            want["avg_scale"] = want["sq_scale"] = (np.uint8, total // B.MX8_BLOCK)
+        for k, (kind, n) in want.items():
+            a = np.asarray(sd[k])
+            if a.dtype != kind or a.shape != (n,):
+                raise ValueError(f"{k}: expected {np.dtype(kind).name}[{n}], got {a.dtype}{list(a.shape)}")
+        with torch.cuda.device(self.device):
+            arr = {k: torch.from_numpy(np.ascontiguousarray(sd[k])).to(self.device) for k in want}
+            at = 0
+            for i, (m, n) in enumerate(zip(self.masters, self.numels)):
+                m.detach().view(-1).copy_(arr["master"][at:at + n])
+                if self.params is not None:
+                    self.params[i].detach().copy_(m.detach())
+                at += n
+            for k, scale, root in (("exp_avg", "avg_scale", False), ("exp_avg_sq", "sq_scale", True)):
+                mine = getattr(self, k)
+                if mx and self.state_bits == 8:
+                    mine.view(torch.uint8).copy_(arr[k])
+                    getattr(self, scale).view(torch.uint8).copy_(arr[scale])
+                elif mx:
+                    B.mx8_decode(arr[k], arr[scale], mine, root=root)
+                elif self.state_bits == 8:
+                    B.mx8_encode(arr[k], mine, getattr(self, scale), root=root, rounding="nearest")
+                else:
+                    mine.copy_(arr[k])
+            self._write_control(B.ctl_from_bytes(raw))
+            torch.cuda.synchronize(self.device)
+
+    def save(self, path: str):
+        """Writes state_dict() to a .npz file (plain arrays, no pickles)."""
+        import numpy as np
+        np.savez(path, **self.state_dict())
+
+    def load(self, path: str):
+        """Restores a file written by save() (loaded without pickles)."""
+        import numpy as np
+        with np.load(path, allow_pickle=False) as z:
+            self.load_state_dict({k: z[k] for k in z.files})
