@@ -554,11 +554,13 @@ int zero_tensors_grad_norm(const zero_tensor_list* list, const void* table, doub
                            const zero_step_ctl* ctl, int32_t* overflow, double* sumsq, void* workspace,
                            void* stream);
 
-/* One Adam/AdamW step of every tensor of the list, in place, in one launch:
- * the float64 sequence of zero_adam_step on g = raw * (coef / L), m', v' and
- * p' rounded to fp32; with 8-bit states fp32(m') and the fp32 square root
- * of fp32(v') are then encoded (zero_mx8_encode), and read back as
- * zero_mx8_decode does.  The step number and the beta powers are ctl's; the
+/* One Adam/AdamW step of every tensor of the list, in place, in one launch.
+ * fp32 states: the float64 sequence of zero_adam_step on g = raw * (coef / L),
+ * m', v' and p' rounded to fp32.  8-bit states, read as zero_mx8_decode does:
+ * m' and v' of the same sequence rounded to fp32, then m' and r = fp32(sqrt(v'))
+ * encoded as zero_mx8_encode does, and the update in fp32 arithmetic, p' =
+ * p - (lr wd p + lr/(1-b1^t) m' / (r / sqrt(1-b2^t) + eps)), eps not below
+ * 2^-126 (off by at most 12 * 2^-24 of the update's terms and the rounding of p').  The step number and the beta powers are ctl's; the
  * launch's last workgroup commits the step there (t += 1; `cur` is not
  * used).
  *   overflow: device flag of zero_tensors_grad_norm; nonzero skips the step:

@@ -1,9 +1,15 @@
 """The tensor-list operators on the GPU against the oracle (float64
 arithmetic, fp32 or 8-bit storage).
 
-Weights and states are compared bit for bit: both sides take the same IEEE
-float64 operations in the same order and round once (RNE) to fp32, and the
-8-bit form is defined to the last bit.  The sum of squares is compared
+States, and weights beside fp32 states, are compared bit for bit: both sides
+take the same IEEE float64 operations in the same order and round once (RNE)
+to fp32, and the 8-bit form is defined to the last bit.  Weights beside 8-bit
+states are updated in fp32: p' = p - u, u = lr wd p + ss q, q = m' / d.  In
+steps of 2^-24 relative (half a step of an fp32 rounding): the root 1.5 (its
+own rounding and half of v's), d 2 more (1/sqrt(1-b2^t) and the fused
+multiply-add), its reciprocal 2, the product and m' 2, ss and its product 2,
+lr wd and the last fused multiply-add 2: u is off by at most 12 steps of |ss
+q| + |lr wd p|, and each side rounds p' by one step of it.  The sum of squares is compared
 within 64 * 2^-53 relative: at these sizes a sum of non-negative terms
 passes at most 16 additions in a lane, 9 in its workgroup, 8 + 9 over the
 workgroups' parts and 2 products, each off by at most 2^-53 relative.
@@ -105,6 +111,7 @@ class Lists:
         self.sq = torch.zeros(1, dtype=torch.float64, device="cuda")
         self.hp = B.adam_hp(*(args[k] for k in ("lr", "beta1", "beta2", "eps", "weight_decay")), self.clip,
                             **self.scaler)
+        self.far = [np.zeros(n) for n in sizes] if bits8 else None
         self.ref = to.TensorAdam(p0, 8 if bits8 else 32, **args, stochastic=self.rounding == "stochastic",
                                  seed=self.seed, flat_offs=flat_offs)
 
@@ -119,6 +126,15 @@ class Lists:
             t.copy_(d)
             hosts.append(h)
         return hosts
+
+    def _widen(self, old):
+        """The bound on the 8-bit lists' weights after one more step from
+        ``old`` (the oracle's weights); |ss q| <= |u| + |lr wd p|."""
+        lr, wd = self.hp.lr, self.hp.weight_decay
+        for i, (a, b) in enumerate(zip(old, self.ref.p)):
+            a, b = np.abs(a.astype(np.float64)), np.abs(b.astype(np.float64))
+            u = np.abs(old[i].astype(np.float64) - self.ref.p[i].astype(np.float64)) + 2.0 ** -24 * (a + b)
+            self.far[i] = self.far[i] + 2.0 ** -24 * (12 * (u + 2 * lr * wd * a) + 2 * b)
 
     def control(self):
         return self.B.ctl_from_bytes(bytes(self.ctl.cpu().numpy().tobytes()))
@@ -142,7 +158,11 @@ class Lists:
                 assert abs(sq - want) <= 64 * 2.0 ** -53 * want
         coef = min(1.0, self.clip / (np.sqrt(sq) + 1e-6)) if self.clip > 0 and not ovf else 1.0
         if not ovf:
-            self.ref.step(hosts, scale, coef)
+            old = [x.copy() for x in self.ref.p]
+            with np.errstate(invalid="ignore"):
+                self.ref.step(hosts, scale, coef)
+                if self.far is not None:
+                    self._widen(old)
         ctl = self.control()
         assert (ctl["t"], ctl["overflow"], ctl["cur"]) == (self.ref.t, ovf, 0)
         assert (ctl["beta1_pow"], ctl["beta2_pow"]) == (self.ref.b1p, self.ref.b2p)
@@ -156,9 +176,13 @@ class Lists:
         torch = self.torch
         for i, n in enumerate(self.sizes):
             at = (what, i, n)
-            assert np.array_equal(bits(self.p[i]), self.ref.p[i].view(np.uint32)), ("master", at)
+            if self.far is None:
+                assert np.array_equal(bits(self.p[i]), self.ref.p[i].view(np.uint32)), ("master", at)
+            else:
+                off = np.abs(self.p[i].cpu().numpy().astype(np.float64) - self.ref.p[i])
+                assert (off <= self.far[i]).all(), ("master", at, off.max())
             if self.w is not None:
-                want = torch.from_numpy(self.ref.p[i]).to(self.w[i].dtype)
+                want = self.p[i].cpu().to(self.w[i].dtype)
                 assert torch.equal(self.w[i].cpu().view(torch.int16), want.view(torch.int16)), ("param", at)
             for mine, scale, ref, name in ((self.m, self.ms, self.ref.m, "m"), (self.v, self.vs, self.ref.v, "v")):
                 if scale is None:
@@ -385,7 +409,10 @@ def test_unchecked_inf_stays_in_its_block():
             lo, hi = (64, 96) if bits8 else (70, 71)
             assert bad.tolist() == ([] if i == 0 else list(range(lo, hi)))
             ok = np.isfinite(p)
-            assert np.array_equal(p[ok], x.ref.p[i][ok])
+            if bits8:
+                assert (np.abs(p[ok].astype(np.float64) - x.ref.p[i][ok]) <= x.far[i][ok]).all()
+            else:
+                assert np.array_equal(p[ok], x.ref.p[i][ok])
         if bits8:
             assert bits(x.ms[1])[2] == 255 and bits(x.vs[1])[2] == 255
         assert x.arena.gaps_intact()
@@ -441,8 +468,9 @@ def test_same_as_the_fused_step():
 
 @pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
 def test_8_bit_step_is_decode_step_encode(rounding):
-    """The 8-bit step equals the 32-bit step between a decode and an encode
-    of the same arrays, bit for bit."""
+    """The 8-bit step leaves the states of a 32-bit step between a decode and
+    an encode of the same arrays, bit for bit (its weights are compared with
+    the oracle's elsewhere)."""
     torch = torch_mod()
     from zero_partitioned_mixed_buffer_amd import TensorAdam, mx8_decode, mx8_encode
     g = torch.Generator(device="cuda").manual_seed(4)
@@ -457,7 +485,9 @@ def test_8_bit_step_is_decode_step_encode(rounding):
         mx8_decode(a.exp_avg_sq, a.sq_scale, b.exp_avg_sq, root=True)
         a.step()
         b.step()
-        assert torch.equal(p8, p32)
+        # 12 * 2^-24 of an update below 0.01, and 2 * 2^-24 of weights below 0.12
+        assert float((p8 - p32).abs().max()) <= 2.0 ** -24 * (12 * 0.01 + 2 * 0.12)
+        p32.copy_(p8)
         for x, codes, scales, root in ((b.exp_avg, a.exp_avg, a.avg_scale, False),
                                        (b.exp_avg_sq, a.exp_avg_sq, a.sq_scale, True)):
             c, s = torch.zeros_like(codes.view(torch.uint8)), torch.ones_like(scales.view(torch.uint8))
@@ -628,9 +658,9 @@ def test_checkpoint_between_widths():
 @pytest.mark.parametrize("state_bits", [8, 32])
 def test_past_the_int32_range(state_bits):
     """One tensor of 2^31 + 4163 elements: the elements around 2^31 and at the
-    end step as the same elements in a short list with the same counters (spans of
-    whole
-    blocks, but for the last: a block cut short would have its own scale)."""
+    end step as the same elements in a short list with the same counters
+    (spans of whole blocks, but for the last: a block cut short would have
+    its own scale)."""
     torch = torch_mod()
     from zero_partitioned_mixed_buffer_amd import TensorAdam
     n = 2 ** 31 + 4163

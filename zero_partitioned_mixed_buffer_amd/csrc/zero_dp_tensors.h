@@ -16,6 +16,13 @@ namespace zdp {
 constexpr int kChunk = 4096;
 constexpr int kMxBlock = 32;  // elements that share a scale in the 8-bit form
 
+// Counters of the operators' tickets, beside the workspace's first: in the
+// bytes between its element count and its partial sums.  As there, every
+// call leaves them at zero.
+constexpr int64_t kWsSubTickets = 128;
+constexpr uint32_t kSubTickets = 32;
+static_assert(kWsRunCount + 8 <= kWsSubTickets && kWsSubTickets + 4 * kSubTickets <= kWsPartSq, "workspace layout");
+
 // Device table of a list: the tensors' descriptors, then one reference per
 // chunk, in list order.
 struct TensorDesc {

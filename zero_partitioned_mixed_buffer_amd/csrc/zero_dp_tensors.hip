@@ -8,8 +8,13 @@
 //              m' = b1*m + (1-b1)*g          v' = b2*v + (1-b2)*(g*g)
 //              d  = sqrt(v') * (1/sqrt(1-b2^t)) + eps
 //              p' = p*(1-lr*wd) - (lr/(1-b1^t)) * (m'/d)
-//            one IEEE float64 operation at a time, state stored as fp32, or
-//            as 8 bits: fp32(m') and sqrt(fp32(v')) encoded as below
+//            fp32 states: one IEEE float64 operation at a time, rounded once
+//            to fp32.  8-bit states: m' and v' as above, rounded to fp32; r =
+//            sqrt(v'); m' and r encoded as below, and the update in fp32:
+//              p' = p - (lr*wd*p + lr/(1-b1^t) * m' / (r/sqrt(1-b2^t) + eps))
+//            (the states carry 4 significant bits, so the update term needs
+//            no more than fp32's 24; the codes come from the float64 sums,
+//            which puts a value beside a border on the right side)
 //   encode   blocks of 32 fp32 values: scale 2^(e-127) with the smallest e >= 1
 //            that keeps the largest magnitude within 448 scales, each value
 //            over the scale in e4m3 (nearest, or stochastic: the random word's
@@ -38,6 +43,8 @@ using zdp::ListArgs;
 using zdp::Partials;
 using zdp::TensorDesc;
 using zdp::TensorStepArgs;
+
+constexpr uint32_t kSubTickets = zdp::kSubTickets;
 
 // Elements per lane per row of a chunk: a 16-byte fp32 vector, an 8-byte
 // 16-bit vector, a 4-byte vector of codes.  Tensors need only their
@@ -101,6 +108,24 @@ __device__ __forceinline__ uint32_t max8(uint32_t x) {
     return x;
 }
 
+// Draws a ticket for the workgroup (one thread of it): true for the last of
+// the grid, which leaves the counters at zero.  Draws on one address follow
+// each other at about 10 ns, so the workgroups draw from 32 counters, and
+// the last of each draws from the one behind them (600 workgroups: 16.0 us
+// of kernel on one counter, 12.5 on 33).  The order is relaxed: what has
+// to be seen by the last workgroup has to be performed before the draw.
+__device__ __forceinline__ bool last_to_draw(uint32_t* ticket) {
+    const uint32_t s = blockIdx.x % kSubTickets;
+    const uint32_t members = (gridDim.x - s + kSubTickets - 1) / kSubTickets;
+    uint32_t* const sub = ticket + (zdp::kWsSubTickets - zdp::kWsTicket) / 4 + s;
+    if (__hip_atomic_fetch_add(sub, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != members - 1) return false;
+    __hip_atomic_store(sub, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t subs = gridDim.x < kSubTickets ? gridDim.x : kSubTickets;
+    if (__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != subs - 1) return false;
+    __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
 // ------------------------------------------------------------- random bits
 // A 32-bit mixing function: two odd multiplications between folds.  The
 // multipliers are the best of 60 random pairs by how evenly one input bit
@@ -150,48 +175,95 @@ __device__ __forceinline__ fvec decode4(uint32_t codes, float scale) {
     return r;
 }
 
-// The four codes of x, whose block (8 lanes) may lie in any part of the
-// wave: all lanes have to be here, with zeros for elements that are not.
-// The conversions take the scale as an operand.  Their stochastic form adds
-// the top 20 bits of its random operand to the mantissa's last 20 bits and
-// cuts them off, counted in the target's subnormal steps below 2^-6.
-template <bool kRoot>
-__device__ __forceinline__ uint32_t encode4(const fvec& x, bool stochastic, const uint32_t (&word)[kV],
-                                            uint32_t& byte) {
-    uint32_t big = 0;
+__device__ __forceinline__ uint32_t bits_of(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float float_of(uint32_t x) { return __builtin_bit_cast(float, x); }
+
+// Correctly rounded square roots of four fp32 values.  The hardware's root s
+// is off by at most one step u; x lies above the midpoint (s - u/2)^2 =
+// s (s - u) + u^2/4 exactly where x > s (s - u), since both sides of that are
+// multiples of a unit larger than u^2/4, and likewise at s + u/2; one fused
+// multiply-add gives the sign.  Nothing underflows in it from 2^-96 up (and
+// at 0); a wave that holds a smaller value takes the library's root, which
+// scales first.
+__device__ __forceinline__ void roots4(fvec& x) {
+    uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
-    for (int e = 0; e < kV; ++e) big = max(big, __builtin_bit_cast(uint32_t, static_cast<float>(x[e])) & 0x7FFFFFFFu);
-    big = max8(big);
-    byte = scale_byte(big);
-    if (byte == 255u) return 0x7F7F7F7Fu;
-    const float scale = __builtin_bit_cast(float, byte << 23);
-    fvec y = x;
-    if (kRoot) {
-        // a positive root keeps at least the smallest code: rounded to zero
-        // it would turn its weight's next update into m/eps
-        const float least = scale * 0x1p-9f;
+    for (int e = 0; e < kV; ++e) least = min(least, bits_of(x[e]) - 1u);
+    if (__any(least < bits_of(0x1p-96f) - 1u)) {
 #pragma unroll
-        for (int e = 0; e < kV; ++e) y[e] = y[e] > 0.0f && y[e] < least ? least : static_cast<float>(y[e]);
+        for (int e = 0; e < kV; ++e) x[e] = __builtin_sqrtf(x[e]);
+        return;
     }
-    if (stochastic) {
+#pragma unroll
+    for (int e = 0; e < kV; ++e) {
+        const float s = __builtin_amdgcn_sqrtf(x[e]);
+        const float down = float_of(bits_of(s) - 1u), up = float_of(bits_of(s) + 1u);
+        const bool lower = __builtin_fmaf(-down, s, x[e]) <= 0.0f, upper = __builtin_fmaf(-up, s, x[e]) > 0.0f;
+        x[e] = upper ? up : lower ? down : s;
+    }
+}
+
+// The four codes of x under their block's scale byte.  The conversions take
+// the scale as an operand.  Their stochastic form adds the top 20 bits of
+// its random operand to the mantissa's last 20 bits and cuts them off,
+// counted in the target's subnormal steps below 2^-6.
+template <bool kStoch>
+__device__ __forceinline__ uint32_t codes4(const fvec& x, float scale, const uint32_t (&bits)[kV]) {
+    if (kStoch) {
         int c = 0;
-        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, y[0], kRoot ? word[0] << 16 : word[0], scale, 0);
-        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, y[1], kRoot ? word[1] << 16 : word[1], scale, 1);
-        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, y[2], kRoot ? word[2] << 16 : word[2], scale, 2);
-        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, y[3], kRoot ? word[3] << 16 : word[3], scale, 3);
+        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, x[0], bits[0], scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, x[1], bits[1], scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, x[2], bits[2], scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, x[3], bits[3], scale, 3);
         return static_cast<uint32_t>(c);
     }
     typedef short s16x2 __attribute__((ext_vector_type(2)));
     s16x2 c = {0, 0};
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, y[0], y[1], scale, false);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, y[2], y[3], scale, true);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, x[0], x[1], scale, false);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, x[2], x[3], scale, true);
     return __builtin_bit_cast(uint32_t, c);
+}
+
+// Encodes a lane's four elements of a block (8 lanes, all of them here, with
+// zeros for elements that are not).  kRoot: x >= 0 are variances, encoded by
+// their square roots, which replace them.
+template <bool kRoot, bool kStoch>
+__device__ __forceinline__ uint32_t encode4(fvec& x, const uint32_t (&word)[kV], uint32_t& byte) {
+    uint32_t big;
+    uint32_t bits[kV];
+    fvec y;
+    if (kRoot) {
+        const fvec v = x;
+        roots4(x);
+        big = max8(max(max(bits_of(x[0]), bits_of(x[1])), max(bits_of(x[2]), bits_of(x[3]))) & 0x7FFFFFFFu);
+        byte = scale_byte(big);
+        // a positive root keeps at least the smallest code: rounded to zero
+        // it would turn its weight's next update into m/eps
+        const float least = __builtin_bit_cast(float, byte << 23) * 0x1p-9f;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+            y[e] = v[e] > 0.0f ? __builtin_fmaxf(x[e], least) : static_cast<float>(x[e]);
+            bits[e] = word[e] << 16;
+        }
+    } else {
+        big = 0;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+            big = max(big, bits_of(x[e]) & 0x7FFFFFFFu);
+            bits[e] = word[e];
+            y[e] = x[e];
+        }
+        big = max8(big);
+        byte = scale_byte(big);
+    }
+    const uint32_t c = codes4<kStoch>(y, __builtin_bit_cast(float, byte << 23), bits);
+    return byte == 255u ? 0x7F7F7F7Fu : c;
 }
 
 // ------------------------------------------------------- loads and stores
 // A lane's kV elements of an array at element j of n; a row that is not
 // `full` is loaded and stored element by element, with zeros for the
-// elements past n.
+// elements past n (a lane at the end of a tensor).
 template <bool kFull>
 __device__ __forceinline__ fvec load_f32(gcf32 p, int j, int n) {
     if (kFull) return ldg(reinterpret_cast<ZDP_GLOBAL const fvec*>(p + j));
@@ -258,6 +330,7 @@ __device__ __forceinline__ void store_8(gu8 p, int j, int n, uint32_t x) {
 template <int kType>
 struct GradVec {
     hvec h;
+    __device__ __forceinline__ void zero() { h = hvec{0, 0}; }
     __device__ __forceinline__ double at(int e) const {
         const uint32_t w = h[e >> 1];
         if (kType == ZERO_TYPE_BF16)
@@ -273,6 +346,7 @@ struct GradVec {
 template <>
 struct GradVec<ZERO_TYPE_F32> {
     fvec f;
+    __device__ __forceinline__ void zero() { f = fvec{0.0f, 0.0f, 0.0f, 0.0f}; }
     __device__ __forceinline__ double at(int e) const { return static_cast<double>(static_cast<float>(f[e])); }
     template <bool kFull>
     __device__ __forceinline__ void load(gcu8 p, int j, int n) {
@@ -333,13 +407,13 @@ __global__ void __launch_bounds__(kBlock) tensors_norm_kernel(ListArgs list, dou
         const int n = at.count();
         const gcu8 g = at.bytes(at.desc->g, grad_size<kGrad>());
         GradVec<kGrad> v[kRows];
-        const int full = n / kRow;
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
             const int j = k * kRow + static_cast<int>(threadIdx.x) * kV;
-            if (k < full)
+            v[k].zero();
+            if (j + kV <= n)
                 v[k].template load<true>(g, j, n);
-            else
+            else if (j < n)
                 v[k].template load<false>(g, j, n);
         }
 #pragma unroll
@@ -354,17 +428,23 @@ __global__ void __launch_bounds__(kBlock) tensors_norm_kernel(ListArgs list, dou
     // the last workgroup sums the workgroups' parts in a fixed order
     __shared__ int s_last;
     sq = block_sum(sq);
+    // (an agent-scope release would write back the XCD's whole L2, once per
+    // workgroup, 80 us a launch of 2048: the part goes out by an exchange
+    // instead, whose returned value says that it has been performed before
+    // the ticket is drawn)
+    uint64_t* const parts = reinterpret_cast<uint64_t*>(ws.sq);
     if (threadIdx.x == 0) {
-        ws.sq[blockIdx.x] = sq;
-        const uint32_t prev = __hip_atomic_fetch_add(ws.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = prev == gridDim.x - 1;
+        uint64_t done = __hip_atomic_exchange(parts + blockIdx.x, __builtin_bit_cast(uint64_t, sq), __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("" : "+v"(done) : : "memory");
+        s_last = last_to_draw(ws.ticket);
     }
     __syncthreads();
     if (!s_last) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     double t = 0.0;
     for (uint32_t i = threadIdx.x; i < gridDim.x; i += kBlock)
-        t += __hip_atomic_load(ws.sq + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        t += __builtin_bit_cast(double, __hip_atomic_load(parts + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     t = block_sum(t);
     if (threadIdx.x == 0) {
         // any inf or NaN among the gradients, or a loss scale without a
@@ -373,7 +453,6 @@ __global__ void __launch_bounds__(kBlock) tensors_norm_kernel(ListArgs list, dou
         const double total = t * (inv * inv);
         *sumsq = total;
         *overflow = __builtin_isfinite(total) ? 0 : 1;
-        __hip_atomic_store(ws.ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
@@ -381,6 +460,7 @@ __global__ void __launch_bounds__(kBlock) tensors_norm_kernel(ListArgs list, dou
 // Scalars of the step taken, t = committed + 1.
 struct AdamScalars {
     double b1, b2, omb1, omb2, ss, isb, dcy, eps, factor;
+    float ssf, isbf, lrwdf, epsf;
 };
 
 __device__ __forceinline__ double clip_coef(const TensorStepArgs& a) {
@@ -400,6 +480,10 @@ __device__ __forceinline__ AdamScalars step_scalars(const TensorStepArgs& a) {
     c.isb = 1.0 / __builtin_sqrt(1.0 - ctl->beta2_pow * a.b2);
     c.dcy = 1.0 - a.lr * a.wd;
     c.eps = a.eps;
+    c.ssf = static_cast<float>(c.ss);
+    c.isbf = static_cast<float>(c.isb);
+    c.lrwdf = static_cast<float>(a.lr * a.wd);
+    c.epsf = __builtin_fmaxf(static_cast<float>(a.eps), 0x1p-126f);
     c.factor = clip_coef(a) * (a.interval > 0 ? 1.0 / ctl->loss_scale : a.inv_scale);
     return c;
 }
@@ -478,106 +562,177 @@ struct Row {
     uint32_t mc, vc, mb, vb;  // 8-bit states: codes and scale bytes
 
     template <bool kFull>
-    __device__ __forceinline__ void load(const Chunk& k, int j) {
+    __device__ __forceinline__ void load_part(const Chunk& k, int j) {
         g.template load<kFull>(k.g, j, k.n);
         p = load_f32<kFull>(reinterpret_cast<gcf32>(k.p), j, k.n);
         if (kMx) {
             mc = load_8<kFull>(k.m, j, k.n);
             vc = load_8<kFull>(k.v, j, k.n);
-            const bool in = kFull || j < k.n;
-            mb = in ? k.ms[j / zdp::kMxBlock] : 1u;
-            vb = in ? k.vs[j / zdp::kMxBlock] : 1u;
+            mb = k.ms[j / zdp::kMxBlock];
+            vb = k.vs[j / zdp::kMxBlock];
         } else {
             m = load_f32<kFull>(reinterpret_cast<gcf32>(k.m), j, k.n);
             v = load_f32<kFull>(reinterpret_cast<gcf32>(k.v), j, k.n);
         }
     }
 
+    // kFull: the row lies inside the chunk; else a lane that is past the
+    // end has zeros (and scale bytes of a block of zeros).
+    template <bool kFull>
+    __device__ __forceinline__ void load(const Chunk& k, int j) {
+        if (kFull) {
+            load_part<true>(k, j);
+            return;
+        }
+        g.zero();
+        p = m = v = fvec{0.0f, 0.0f, 0.0f, 0.0f};
+        mc = vc = 0;
+        mb = vb = 1;
+        if (j + kV <= k.n)
+            load_part<true>(k, j);
+        else if (j < k.n)
+            load_part<false>(k, j);
+    }
+
     template <bool kFull, int kParam>
-    __device__ __forceinline__ void finish(const Chunk& k, int j, const AdamScalars& c, bool stochastic,
-                                           const RandomKey& key) {
+    __device__ __forceinline__ void store_part(const Chunk& k, int j, const fvec& po, const fvec& mo, const fvec& vo,
+                                               uint32_t m4, uint32_t v4) {
         if (kMx) {
-            m = decode4(mc, scale_value(mb));
-            v = decode4(vc, scale_value(vb));
-            v = v * v;
-        }
-        fvec po, mo, vo;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            float a, b, d;
-            adam1(c, g.at(e) * c.factor, p[e], m[e], v[e], a, b, d);
-            po[e] = a;
-            mo[e] = b;
-            vo[e] = d;
-        }
-        store_f32<kFull>(reinterpret_cast<gf32>(k.p), j, k.n, po);
-        if (kParam != ZERO_TYPE_NONE) store_16<kFull>(reinterpret_cast<gu16>(k.w), j, k.n, pack_param<kParam>(po));
-        if (kMx) {
-            uint32_t word[kV] = {0, 0, 0, 0};
-            if (stochastic) {
-#pragma unroll
-                for (int e = 0; e < kV; ++e) word[e] = random_word(key, k.counter + static_cast<uint32_t>(j + e));
-            }
-#pragma unroll
-            for (int e = 0; e < kV; ++e) {
-                const bool in = kFull || j + e < k.n;  // elements past the end count as zeros
-                mo[e] = in ? static_cast<float>(mo[e]) : 0.0f;
-                vo[e] = in ? __builtin_sqrtf(vo[e]) : 0.0f;
-            }
-            uint32_t mbyte, vbyte;
-            const uint32_t m4 = encode4<false>(mo, stochastic, word, mbyte);
-            const uint32_t v4 = encode4<true>(vo, stochastic, word, vbyte);
             store_8<kFull>(k.m, j, k.n, m4);
             store_8<kFull>(k.v, j, k.n, v4);
-            if ((threadIdx.x & 7) == 0 && (kFull || j < k.n)) {
-                k.ms[j / zdp::kMxBlock] = static_cast<uint8_t>(mbyte);
-                k.vs[j / zdp::kMxBlock] = static_cast<uint8_t>(vbyte);
-            }
         } else {
             store_f32<kFull>(reinterpret_cast<gf32>(k.m), j, k.n, mo);
             store_f32<kFull>(reinterpret_cast<gf32>(k.v), j, k.n, vo);
         }
+        store_f32<kFull>(reinterpret_cast<gf32>(k.p), j, k.n, po);
+        if (kParam != ZERO_TYPE_NONE) store_16<kFull>(reinterpret_cast<gu16>(k.w), j, k.n, pack_param<kParam>(po));
+    }
+
+    template <bool kFull, int kParam, bool kStoch>
+    __device__ __forceinline__ void finish(const Chunk& k, int j, const AdamScalars& c, const RandomKey& key) {
+        fvec po, mo, vo;
+        uint32_t m4 = 0, v4 = 0;
+        if (kMx) {
+            m = decode4(mc, scale_value(mb));
+            v = decode4(vc, scale_value(vb));
+            v = v * v;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                const double g1 = g.at(e) * c.factor;
+                const double m1 = (c.b1 * static_cast<double>(m[e])) + (c.omb1 * g1);
+                const double v1 = (c.b2 * static_cast<double>(v[e])) + (c.omb2 * (g1 * g1));
+                mo[e] = static_cast<float>(m1);
+                vo[e] = static_cast<float>(v1);
+            }
+            uint32_t word[kV] = {0, 0, 0, 0};
+            if (kStoch) {
+#pragma unroll
+                for (int e = 0; e < kV; ++e) word[e] = random_word(key, k.counter + static_cast<uint32_t>(j + e));
+            }
+            uint32_t mbyte, vbyte;
+            m4 = encode4<false, kStoch>(mo, word, mbyte);
+            v4 = encode4<true, kStoch>(vo, word, vbyte);  // vo: now the roots
+            if ((threadIdx.x & 7) == 0 && (kFull || j < k.n)) {
+                k.ms[j / zdp::kMxBlock] = static_cast<uint8_t>(mbyte);
+                k.vs[j / zdp::kMxBlock] = static_cast<uint8_t>(vbyte);
+            }
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                const float q = mo[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(vo[e], c.isbf, c.epsf));
+                po[e] = p[e] - __builtin_fmaf(c.lrwdf, p[e], c.ssf * q);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                float a, b, d;
+                adam1(c, g.at(e) * c.factor, p[e], m[e], v[e], a, b, d);
+                po[e] = a;
+                mo[e] = b;
+                vo[e] = d;
+            }
+        }
+        if (kFull || j + kV <= k.n)
+            store_part<true, kParam>(k, j, po, mo, vo, m4, v4);
+        else if (j < k.n)
+            store_part<false, kParam>(k, j, po, mo, vo, m4, v4);
     }
 };
 
-template <int kGrad, int kParam, bool kMx>
+// All rows of a chunk.
+template <int kGrad, bool kMx>
+__device__ __forceinline__ void load_chunk(Row<kGrad, kMx> (&r)[kRows], const Chunk& k) {
+    const int j = static_cast<int>(threadIdx.x) * kV;
+    if (k.n == kChunk) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) r[u].template load<true>(k, j + u * kRow);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) r[u].template load<false>(k, j + u * kRow);
+    }
+}
+
+template <int kGrad, int kParam, bool kMx, bool kStoch>
+__device__ __forceinline__ void finish_chunk(Row<kGrad, kMx> (&r)[kRows], const Chunk& k, const AdamScalars& c,
+                                             const RandomKey& key) {
+    const int j = static_cast<int>(threadIdx.x) * kV;
+    if (k.n == kChunk) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) r[u].template finish<true, kParam, kStoch>(k, j + u * kRow, c, key);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (u * kRow < k.n) r[u].template finish<false, kParam, kStoch>(k, j + u * kRow, c, key);
+    }
+}
+
+template <int kGrad, int kParam, bool kMx, bool kStoch, bool kPipe>
 __global__ void __launch_bounds__(kBlock) tensors_adam_kernel(ListArgs list, TensorStepArgs a) {
     const bool skip = a.overflow != nullptr && *a.overflow != 0;
     if (!skip) {
+        Row<kGrad, kMx> r[kRows];
+        Chunk k;
+        int64_t i = blockIdx.x;
+        if (i < list.n_chunks) {
+            k = chunk_at<kGrad, kMx>(list, i);
+            load_chunk(r, k);
+        }
         const AdamScalars c = step_scalars(a);
         const RandomKey key = random_key(a.seed, static_cast<uint32_t>(a.ctl->t) + 1u);
-        for (int64_t i = blockIdx.x; i < list.n_chunks; i += gridDim.x) {
-            const Chunk k = chunk_at<kGrad, kMx>(list, i);
-            for (int row = 0; row * kRow < k.n; ++row) {
-                const int j = row * kRow + static_cast<int>(threadIdx.x) * kV;
-                Row<kGrad, kMx> r;
-                if ((row + 1) * kRow <= k.n) {
-                    r.template load<true>(k, j);
-                    r.template finish<true, kParam>(k, j, c, a.stochastic != 0, key);
-                } else {
-                    r.template load<false>(k, j);
-                    r.template finish<false, kParam>(k, j, c, a.stochastic != 0, key);
+        while (i < list.n_chunks) {
+            const int64_t i2 = i + gridDim.x;
+            if (kPipe) {
+                Chunk k2 = k;
+                Row<kGrad, kMx> r2[kRows];
+                if (i2 < list.n_chunks) {
+                    k2 = chunk_at<kGrad, kMx>(list, i2);
+                    load_chunk(r2, k2);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                finish_chunk<kGrad, kParam, kMx, kStoch>(r, k, c, key);
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) r[u] = r2[u];
+                k = k2;
+            } else {
+                finish_chunk<kGrad, kParam, kMx, kStoch>(r, k, c, key);
+                if (i2 < list.n_chunks) {
+                    k = chunk_at<kGrad, kMx>(list, i2);
+                    load_chunk(r, k);
                 }
             }
+            i = i2;
         }
     }
     // the last workgroup commits: every workgroup has read the control
     // block by the barrier before its ticket, and nothing it wrote is read
     // here, so the ticket orders no other memory
     __syncthreads();
-    if (threadIdx.x == 0) {
-        const uint32_t prev = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (prev == gridDim.x - 1) {
-            commit(a, skip);
-            __hip_atomic_store(a.ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-    }
+    if (threadIdx.x == 0 && last_to_draw(a.ticket)) commit(a, skip);
 }
 
 // ------------------------------------------------------- encode and decode
-template <bool kRoot>
+template <bool kRoot, bool kStoch>
 __global__ void __launch_bounds__(kBlock) mx8_encode_kernel(const float* x_in, int64_t n, uint8_t* codes_out,
-                                                            uint8_t* scales_out, bool stochastic, RandomKey key,
+                                                            uint8_t* scales_out, RandomKey key,
                                                             uint32_t counter) {
     const gcf32 x = (gcf32)x_in;
     const gu8 codes = (gu8)codes_out, scales = (gu8)scales_out;
@@ -585,20 +740,20 @@ __global__ void __launch_bounds__(kBlock) mx8_encode_kernel(const float* x_in, i
          base += static_cast<int64_t>(gridDim.x) * kRow) {
         const int rest = static_cast<int>(n - base < kRow ? n - base : kRow);
         const int j = static_cast<int>(threadIdx.x) * kV;
-        const bool full = rest == kRow;
-        fvec v = full ? load_f32<true>(x + base, j, rest) : load_f32<false>(x + base, j, rest);
+        const bool full = j + kV <= rest;
+        fvec v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (full)
+            v = load_f32<true>(x + base, j, rest);
+        else if (j < rest)
+            v = load_f32<false>(x + base, j, rest);
         uint32_t word[kV] = {0, 0, 0, 0};
-        if (stochastic) {
+        if (kStoch) {
 #pragma unroll
             for (int e = 0; e < kV; ++e)
                 word[e] = random_word(key, counter + static_cast<uint32_t>(base) + static_cast<uint32_t>(j + e));
         }
-        if (kRoot) {
-#pragma unroll
-            for (int e = 0; e < kV; ++e) v[e] = __builtin_sqrtf(v[e]);
-        }
         uint32_t byte;
-        const uint32_t c = encode4<kRoot>(v, stochastic, word, byte);
+        const uint32_t c = encode4<kRoot, kStoch>(v, word, byte);
         if (full)
             store_8<true>(codes + base, j, rest, c);
         else
@@ -617,7 +772,7 @@ __global__ void __launch_bounds__(kBlock) mx8_decode_kernel(const uint8_t* codes
         const int rest = static_cast<int>(n - base < kRow ? n - base : kRow);
         const int j = static_cast<int>(threadIdx.x) * kV;
         if (j >= rest) continue;
-        const bool full = rest == kRow;
+        const bool full = j + kV <= rest;
         const uint32_t c = full ? load_8<true>(codes + base, j, rest) : load_8<false>(codes + base, j, rest);
         fvec v = decode4(c, scale_value(scales[(base + j) / zdp::kMxBlock]));
         if (kRoot) v = v * v;
@@ -663,25 +818,65 @@ int finish_launch() {
     return ZERO_OK;
 }
 
-constexpr int kNormPerCu = 8;
-constexpr int kAdamPerCu = 4;
+// Workgroups per CU of the long kernels; each was timed against its
+// neighbours on the GPT-2 shaped lists.  Grids that are not a multiple of
+// the CU count lose 10 to 30%.
+//   norm: 5 (1.56e9 bf16 gradients: 443 us; 4: 486, 6: 443, 8: 505)
+//   adam, fp32 states: 1 with the next chunk's loads under way (GPT-2 small:
+//     609 us; 2 such: 656, 4 without the loads ahead: 672)
+//   adam, 8-bit states: 3 (a quarter of GPT-2 XL: 1237 us; 2: 1240, 1: 1454)
+constexpr int kNormPerCu = 5;
+constexpr int kAdamPerCu = 1;
+constexpr int kAdamMxPerCu = 3;
+// fp32 states: a list of at most this many chunks per CU takes one workgroup
+// a chunk, all in flight at once (400 tensors, 600 chunks: 14.3 us; 17.1
+// on kAdamPerCu).
+constexpr int kAdamShortPerCu = 4;
 constexpr int kMx8PerCu = 8;
 
-template <int kGrad, bool kMx>
-int adam_for(const ListArgs& list, const TensorStepArgs& a, hipStream_t s) {
-    const int grid = grid_of(list.n_chunks, kAdamPerCu);
-    if (list.param_type == ZERO_TYPE_F16)
-        tensors_adam_kernel<kGrad, ZERO_TYPE_F16, kMx><<<grid, kBlock, 0, s>>>(list, a);
-    else if (list.param_type == ZERO_TYPE_BF16)
-        tensors_adam_kernel<kGrad, ZERO_TYPE_BF16, kMx><<<grid, kBlock, 0, s>>>(list, a);
-    else
-        tensors_adam_kernel<kGrad, ZERO_TYPE_NONE, kMx><<<grid, kBlock, 0, s>>>(list, a);
+template <int kGrad, int kParam>
+int adam_f32(const ListArgs& list, const TensorStepArgs& a, hipStream_t s) {
+    if (list.n_chunks <= static_cast<int64_t>(cu_count()) * kAdamShortPerCu) {
+        const int grid = grid_of(list.n_chunks, kAdamShortPerCu);
+        tensors_adam_kernel<kGrad, kParam, false, false, false><<<grid, kBlock, 0, s>>>(list, a);
+    } else {
+        const int grid = grid_of(list.n_chunks, kAdamPerCu);
+        tensors_adam_kernel<kGrad, kParam, false, false, true><<<grid, kBlock, 0, s>>>(list, a);
+    }
     return finish_launch();
+}
+
+template <int kGrad, int kParam>
+int adam_mx(const ListArgs& list, const TensorStepArgs& a, hipStream_t s) {
+    const int grid = grid_of(list.n_chunks, kAdamMxPerCu);
+    if (a.stochastic)
+        tensors_adam_kernel<kGrad, kParam, true, true, true><<<grid, kBlock, 0, s>>>(list, a);
+    else
+        tensors_adam_kernel<kGrad, kParam, true, false, true><<<grid, kBlock, 0, s>>>(list, a);
+    return finish_launch();
+}
+
+template <int kGrad, int kParam>
+int adam_with(const ListArgs& list, const TensorStepArgs& a, hipStream_t s) {
+    return list.state_type == ZERO_TYPE_MX8 ? adam_mx<kGrad, kParam>(list, a, s) : adam_f32<kGrad, kParam>(list, a, s);
 }
 
 template <int kGrad>
 int adam_of(const ListArgs& list, const TensorStepArgs& a, hipStream_t s) {
-    return list.state_type == ZERO_TYPE_MX8 ? adam_for<kGrad, true>(list, a, s) : adam_for<kGrad, false>(list, a, s);
+    if (list.param_type == ZERO_TYPE_F16) return adam_with<kGrad, ZERO_TYPE_F16>(list, a, s);
+    if (list.param_type == ZERO_TYPE_BF16) return adam_with<kGrad, ZERO_TYPE_BF16>(list, a, s);
+    return adam_with<kGrad, ZERO_TYPE_NONE>(list, a, s);
+}
+
+template <bool kRoot>
+int encode_of(const float* x, int64_t n, uint8_t* codes, uint8_t* scales, bool stochastic, const RandomKey& key,
+              uint32_t counter, hipStream_t s) {
+    const int grid = grid_of((n + kRow - 1) / kRow, kMx8PerCu);
+    if (stochastic)
+        mx8_encode_kernel<kRoot, true><<<grid, kBlock, 0, s>>>(x, n, codes, scales, key, counter);
+    else
+        mx8_encode_kernel<kRoot, false><<<grid, kBlock, 0, s>>>(x, n, codes, scales, key, counter);
+    return finish_launch();
 }
 
 }  // namespace
@@ -711,14 +906,10 @@ int launch_tensors_adam(const ListArgs& list, const TensorStepArgs& a, void* str
 int launch_mx8_encode(const float* x, int64_t n, bool root, uint8_t* codes, uint8_t* scales, bool stochastic,
                       uint64_t seed, uint32_t step, uint64_t flat_off, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const int grid = grid_of((n + kRow - 1) / kRow, kMx8PerCu);
     const RandomKey key = random_key(seed, step);
     const uint32_t counter = static_cast<uint32_t>(flat_off);
-    if (root)
-        mx8_encode_kernel<true><<<grid, kBlock, 0, s>>>(x, n, codes, scales, stochastic, key, counter);
-    else
-        mx8_encode_kernel<false><<<grid, kBlock, 0, s>>>(x, n, codes, scales, stochastic, key, counter);
-    return finish_launch();
+    return root ? encode_of<true>(x, n, codes, scales, stochastic, key, counter, s)
+                : encode_of<false>(x, n, codes, scales, stochastic, key, counter, s);
 }
 
 int launch_mx8_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, bool root, float* x, void* stream) {
