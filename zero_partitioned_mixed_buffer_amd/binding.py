@@ -226,10 +226,20 @@ def _check_ws(ws):
         raise ValueError(f"workspace: a device tensor of at least {workspace_bytes()} bytes")
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None:
+            import torch
+            torch.cuda.init()
+            current, raw = torch.cuda.current_device, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            # the stream's address alone: 0.3 us where a Stream object takes 3
+            _raw_stream = (lambda: raw(current())) if raw else \
+                (lambda: int(torch.cuda.current_stream().cuda_stream))
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -458,14 +468,29 @@ _CODES = ("float8_e4m3fn", "uint8")
 _SCALES = ("float8_e8m0fnu", "uint8")
 
 
-def _check_current(t, what: str):
+def _check_current(t, what: str, cur: Optional[int] = None):
     """A tensor of the current device: the launch goes to that device's stream."""
     if _is_tensor(t):
-        import torch
         if not t.is_cuda:
             raise ValueError(f"{what}: must be a device tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{what}: on {t.device}, but the current device is {torch.cuda.current_device()}")
+        if cur is None:
+            import torch
+            cur = torch.cuda.current_device()
+        if t.get_device() != cur:
+            raise ValueError(f"{what}: on {t.device}, but the current device is {cur}")
+
+
+def _check_operand(t, n: int, kinds: Tuple[str, ...], what: str, cur: int):
+    """_check_span from element 0 and _check_current."""
+    if _is_tensor(t) and not (_dtype_name(t) in kinds and t.numel() >= n and t.get_device() == cur
+                              and t.is_contiguous()):
+        _check_span(t, 0, n, kinds, what)
+        _check_current(t, what, cur)
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
 
 
 def _common_dtype(tensors: Sequence, kinds: Tuple[str, ...], what: str) -> str:
@@ -481,6 +506,7 @@ class TensorList:
 
     def __init__(self, info: TensorListInfo, table, tensors):
         self.info = info
+        self.ref = C.byref(info)
         self.table = table
         self.tensors = tensors
         self.numel = int(info.n_elems)
@@ -570,13 +596,14 @@ def tensor_list(grads: Sequence, masters: Optional[Sequence] = None, params: Opt
 def tensors_grad_norm(lst: TensorList, overflow, sumsq, workspace, loss_scale: float = 1.0, ctl=None, stream=None):
     """sum g^2 of the list's gradients over ``loss_scale`` (or the control
     block's scale) into ``sumsq``, and whether it is not finite into ``overflow``."""
-    for t, kind, what in ((overflow, "int32", "overflow flag"), (sumsq, "float64", "sum of squares")):
-        _check_span(t, 0, 1, (kind,), what)
-        _check_current(t, what)
+    cur = _current_device()
+    _check_operand(overflow, 1, ("int32",), "overflow flag", cur)
+    _check_operand(sumsq, 1, ("float64",), "sum of squares", cur)
     _check_ws(workspace)
+    for t, what in ((workspace, "workspace"), (ctl, "control block"), (lst.table, "tensor list")):
+        _check_current(t, what, cur)
     _check_ctl(ctl)
-    _check_current(lst.table, "tensor list")
-    _check(lib().zero_tensors_grad_norm(C.byref(lst.info), _ptr(lst.table), float(loss_scale), _ptr(ctl),
+    _check(lib().zero_tensors_grad_norm(lst.ref, _ptr(lst.table), float(loss_scale), _ptr(ctl),
                                         _ptr(overflow), _ptr(sumsq), _ptr(workspace), _stream(stream)),
            "zero_tensors_grad_norm")
 
@@ -595,16 +622,14 @@ def _rounding(name: str) -> int:
 def tensors_adam_step(lst: TensorList, hp: AdamHp, ctl, workspace, loss_scale: float = 1.0, overflow=None,
                       sumsq=None, rounding: str = "nearest", seed: int = 0, stream=None):
     """One Adam/AdamW step of every tensor of the list, in place."""
-    if overflow is not None:
-        _check_span(overflow, 0, 1, ("int32",), "overflow flag")
-    if sumsq is not None:
-        _check_span(sumsq, 0, 1, ("float64",), "sum of squares")
+    cur = _current_device()
+    _check_operand(overflow, 1, ("int32",), "overflow flag", cur)
+    _check_operand(sumsq, 1, ("float64",), "sum of squares", cur)
     _check_ws(workspace)
+    for t, what in ((workspace, "workspace"), (ctl, "control block"), (lst.table, "tensor list")):
+        _check_current(t, what, cur)
     _check_ctl(ctl)
-    for t, what in ((overflow, "overflow flag"), (sumsq, "sum of squares"), (ctl, "control block"),
-                    (lst.table, "tensor list")):
-        _check_current(t, what)
-    _check(lib().zero_tensors_adam_step(C.byref(lst.info), _ptr(lst.table), C.byref(hp), float(loss_scale),
+    _check(lib().zero_tensors_adam_step(lst.ref, _ptr(lst.table), C.byref(hp), float(loss_scale),
                                         _ptr(ctl), _ptr(overflow), _ptr(sumsq), _rounding(rounding),
                                         int(seed) & (2**64 - 1), _ptr(workspace), _stream(stream)),
            "zero_tensors_adam_step")
@@ -612,10 +637,10 @@ def tensors_adam_step(lst: TensorList, hp: AdamHp, ctl, workspace, loss_scale: f
 
 def _check_mx8(x, codes, scales):
     n = int(x.numel())
-    for t, off, kinds, what in ((x, n, ("float32",), "array"), (codes, n, _CODES, "codes"),
-                                (scales, -(-n // MX8_BLOCK), _SCALES, "scales")):
-        _check_span(t, 0, off, kinds, what)
-        _check_current(t, what)
+    cur = _current_device()
+    _check_operand(x, n, ("float32",), "array", cur)
+    _check_operand(codes, n, _CODES, "codes", cur)
+    _check_operand(scales, -(-n // MX8_BLOCK), _SCALES, "scales", cur)
     return n
 
 

@@ -76,7 +76,7 @@ class TensorAdam:
         self.loss_scale = float(loss_scale)
         self.check_finite = bool(check_finite)
         self.rounding = rounding if state_bits == 8 else "nearest"
-        self.seed = int(seed)
+        self.seed = int(seed) & (2**64 - 1)
         self._plan()
 
     def _views(self, flat, per=1):
@@ -90,6 +90,11 @@ class TensorAdam:
                                       self._views(self.exp_avg_sq),
                                       self._views(self.avg_scale, B.MX8_BLOCK) if mx else None,
                                       self._views(self.sq_scale, B.MX8_BLOCK) if mx else None, self.flat_offs)
+        # the calls' fixed arguments; every buffer is this object's own
+        table = None if self.list.table is None else self.list.table.data_ptr()
+        self._head = (self.list.ref, table)
+        self._checks = (self.overflow.data_ptr(), self.sumsq.data_ptr()) if self.check_finite else (None, None)
+        self._ctl, self._ws = self.ctl.data_ptr(), self.workspace.data_ptr()
 
     def set_grads(self, grads: Sequence):
         """Other gradient tensors of the same sizes, from the next step on."""
@@ -103,22 +108,17 @@ class TensorAdam:
     def step(self, stream=None):
         """One step on what the gradient tensors hold, scaled by ``loss_scale``
         (with dynamic scaling by the control block's)."""
-        import torch
-        if torch.cuda.current_device() != self.device.index:
+        if B._current_device() != self.device.index:
+            import torch
             with torch.cuda.device(self.device):
                 return self.step(stream)
-        s = B._stream(stream)
-        L, info, table = B.lib(), C.byref(self.list.info), self.list.table
-        table = None if table is None else table.data_ptr()
-        ctl, ws = self.ctl.data_ptr(), self.workspace.data_ptr()
-        overflow = sumsq = None
+        s, L, scale = B._stream(stream), B.lib(), self.loss_scale
         if self.check_finite:
-            overflow, sumsq = self.overflow.data_ptr(), self.sumsq.data_ptr()
-            dyn = ctl if self.hp.scale_interval > 0 else None
-            B._check(L.zero_tensors_grad_norm(info, table, self.loss_scale, dyn, overflow, sumsq, ws, s),
+            dyn = self._ctl if self.hp.scale_interval > 0 else None
+            B._check(L.zero_tensors_grad_norm(*self._head, scale, dyn, *self._checks, self._ws, s),
                      "zero_tensors_grad_norm")
-        B._check(L.zero_tensors_adam_step(info, table, C.byref(self.hp), self.loss_scale, ctl, overflow, sumsq,
-                                          B.ROUNDING[self.rounding], self.seed & (2**64 - 1), ws, s),
+        B._check(L.zero_tensors_adam_step(*self._head, C.byref(self.hp), scale, self._ctl, *self._checks,
+                                          B.ROUNDING[self.rounding], self.seed, self._ws, s),
                  "zero_tensors_adam_step")
 
     def control(self) -> dict:
