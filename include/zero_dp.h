@@ -451,7 +451,7 @@ int zero_gather_layers(const uint16_t* const* windows, int32_t nd, int64_t part,
 /* ---- tensor lists -----------------------------------------------------
  * The optimizer step of parameters that are separate tensors (stage 0, or
  * the tensors and fragments that zero_plan_partitions gives a rank) rather
- * than one flat window: one launch steps the whole list, in place.  Sources
+ * than one flat window, in place, whatever their number and sizes.  Sources
  * as for the fused step: mixed-precision Adam with float32 master weights,
  * momentum and variance (anthology note "Assumptions"; trishampatil "The
  * Real Problem").  The 8-bit states are this library's own; the pages hold
@@ -554,14 +554,16 @@ int zero_tensors_grad_norm(const zero_tensor_list* list, const void* table, doub
                            const zero_step_ctl* ctl, int32_t* overflow, double* sumsq, void* workspace,
                            void* stream);
 
-/* One Adam/AdamW step of every tensor of the list, in place, in one launch.
+/* One Adam/AdamW step of every tensor of the list, in place, in one launch
+ * (a list of more than about 2^27 elements: in launches of about 2^26; where
+ * one of them fails, ZERO_EHIP, the tensors before it may have been stepped).
  * fp32 states: the float64 sequence of zero_adam_step on g = raw * (coef / L),
  * m', v' and p' rounded to fp32.  8-bit states, read as zero_mx8_decode does:
  * m' and v' of the same sequence rounded to fp32, then m' and r = fp32(sqrt(v'))
  * encoded as zero_mx8_encode does, and the update in fp32 arithmetic, p' =
  * p - (lr wd p + lr/(1-b1^t) m' / (r / sqrt(1-b2^t) + eps)), eps not below
  * 2^-126 (off by at most 12 * 2^-24 of the update's terms and the rounding of p').  The step number and the beta powers are ctl's; the
- * launch's last workgroup commits the step there (t += 1; `cur` is not
+ * last launch's last workgroup commits the step there (t += 1; `cur` is not
  * used).
  *   overflow: device flag of zero_tensors_grad_norm; nonzero skips the step:
  *     no tensor is touched, ctl->skipped += 1, the dynamic scale backs off.
