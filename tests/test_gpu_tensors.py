@@ -557,6 +557,31 @@ def test_graph_replays_match_eager_steps(state_bits):
     assert eager[0].control()["skipped"] == 2
 
 
+def test_graph_sees_other_gradients():
+    """A captured step reads the tensors that set_grads named since."""
+    torch = torch_mod()
+    eager, graphed = _adam_pair(8, seed=5)
+    n = eager[2].numel()
+    cut = [0, 33, 5000, n]
+    for o in (eager, graphed):
+        o[0].step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed[0].step()
+    for rep in range(3):
+        x = (torch.randn(n, device="cuda") * 1e-3).bfloat16()
+        eager[0].set_grads([x[i:j] for i, j in zip(cut, cut[1:])])
+        y = x.clone()
+        graphed[0].set_grads([y[i:j] for i, j in zip(cut, cut[1:])])
+        torch.cuda.synchronize()
+        graph.replay()
+        eager[0].step()
+        torch.cuda.synchronize()
+        _same(eager, graphed)
+    assert eager[0].control()["t"] == 4
+
+
 def test_two_streams():
     """Two lists stepped at once on two streams, each with its own workspace."""
     torch = torch_mod()
@@ -604,8 +629,10 @@ def test_other_gradients_and_refusals():
     b.step()
     torch.cuda.synchronize()
     assert torch.equal(pa, pb) and torch.equal(wa, wb)
-    with pytest.raises(ValueError, match="expected"):
-        b.set_grads([x[:10], x[:10], x[:10]])
+    for bad, msg in (([x[:10], x[:10], x[:10]], "expected"), ([g.float() for g in b.grads], "dtype"),
+                     (b.grads[:2], "entries")):
+        with pytest.raises(ValueError, match=msg):
+            b.set_grads(bad)
     assert len(b.grads) == 3 and b.grads[0].numel() == 33
     with pytest.raises(B.ZeroError):
         TensorAdam([pa, pa], [x, x])  # the same weight twice

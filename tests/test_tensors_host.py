@@ -324,6 +324,8 @@ def test_python_refusals():
     g, m = [torch.zeros(4, dtype=torch.float16)], [torch.zeros(4)]
     with pytest.raises(ValueError, match="device tensor"):
         B.tensor_list(g)
+    with pytest.raises(ValueError, match="torch tensors"):
+        B.tensor_list([None])
     with pytest.raises(ValueError, match="come together"):
         B.tensor_list(g, m)
     with pytest.raises(ValueError, match="gradients alone"):

@@ -539,6 +539,8 @@ def tensor_list(grads: Sequence, masters: Optional[Sequence] = None, params: Opt
     for what, col in columns.items():
         if col is not None and len(col) != count:
             raise ValueError(f"{what}: {len(col)} entries for {count} gradients")
+        if col is not None and what != "flat_offs" and not all(isinstance(t, torch.Tensor) for t in col):
+            raise ValueError(f"{what}: torch tensors expected")
     gtype = _LIST_TYPES[_common_dtype(grads, tuple(_LIST_TYPES), "gradients")]
     ptype, stype = TYPE_NONE, TYPE_NONE
     numels = [int(g.numel()) for g in grads]

@@ -82,14 +82,17 @@ class TensorAdam:
     def _views(self, flat, per=1):
         return [flat[o // per:o // per + -(-n // per)] for o, n in zip(self.state_offs, self.numels)]
 
-    def _plan(self):
+    def _tensor_list(self, grads):
         import torch
         mx = self.state_bits == 8
         with torch.cuda.device(self.device):
-            self.list = B.tensor_list(self.grads, self.masters, self.params, self._views(self.exp_avg),
-                                      self._views(self.exp_avg_sq),
-                                      self._views(self.avg_scale, B.MX8_BLOCK) if mx else None,
-                                      self._views(self.sq_scale, B.MX8_BLOCK) if mx else None, self.flat_offs)
+            return B.tensor_list(grads, self.masters, self.params, self._views(self.exp_avg),
+                                 self._views(self.exp_avg_sq),
+                                 self._views(self.avg_scale, B.MX8_BLOCK) if mx else None,
+                                 self._views(self.sq_scale, B.MX8_BLOCK) if mx else None, self.flat_offs)
+
+    def _plan(self):
+        self.list = self._tensor_list(self.grads)
         # the calls' fixed arguments; every buffer is this object's own
         table = None if self.list.table is None else self.list.table.data_ptr()
         self._head = (self.list.ref, table)
@@ -97,13 +100,18 @@ class TensorAdam:
         self._ctl, self._ws = self.ctl.data_ptr(), self.workspace.data_ptr()
 
     def set_grads(self, grads: Sequence):
-        """Other gradient tensors of the same sizes, from the next step on."""
-        old, self.grads = self.grads, list(grads)
-        try:
-            self._plan()
-        except Exception:
-            self.grads = old
-            raise
+        """Other gradient tensors of the same sizes and dtype, from the next
+        step on the current stream (steps under way on other streams have to
+        have ended).  The list's table is rewritten in place, so that steps
+        captured in a graph read the new tensors too."""
+        import torch
+        new = self._tensor_list(list(grads))
+        if new.info.grad_type != self.list.info.grad_type:
+            raise ValueError(f"gradients: dtype {grads[0].dtype}, but the list was planned with {self.grads[0].dtype}")
+        with torch.cuda.device(self.device):
+            if new.table is not None:
+                self.list.table.copy_(new.table)
+        self.list.tensors, self.grads = new.tensors, list(grads)
 
     def step(self, stream=None):
         """One step on what the gradient tensors hold, scaled by ``loss_scale``
