@@ -119,7 +119,7 @@ def grad_norm(grads, loss_scale: float):
         parts = [raw_grad(g) for g in grads]
         finite = all(np.isfinite(x).all() for x in parts)
         total = math.fsum(float(v) for x in parts for v in x * x) if finite else math.inf
-        total = total * (inv * inv) if not (total == 0 and math.isinf(inv)) else math.nan
+        total = total * inv * inv if not (total == 0 and math.isinf(inv)) else math.nan
     return (not math.isfinite(total)), total
 
 

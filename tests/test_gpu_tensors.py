@@ -495,6 +495,41 @@ def test_8_bit_step_is_decode_step_encode(rounding):
             assert torch.equal(c, codes.view(torch.uint8)) and torch.equal(s, scales.view(torch.uint8)), (t, root)
 
 
+def test_two_lists_under_one_norm():
+    """Two groups of tensors clipped by their common norm: as one list."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam
+    torch.manual_seed(9)
+    p = [torch.randn(n, device="cuda") for n in (5000, 333, 70000)]
+    g = [torch.randn(n, device="cuda") for n in (5000, 333, 70000)]
+    q = [x.clone() for x in p]
+    hp = dict(max_grad_norm=2.0, loss_scale=4.0)
+    one = TensorAdam(p, g, **hp)
+    a, b = TensorAdam(q[:2], g[:2], **hp), TensorAdam(q[2:], g[2:], **hp)
+    for t in range(4):
+        if t == 2:
+            g[0][17] = float("nan")
+        one.step()
+        for x in (a, b):
+            x.grad_norm()
+        flag, total = a.overflow | b.overflow, a.sumsq + b.sumsq
+        for x in (a, b):
+            x.step(norm=(flag, one.sumsq))
+        torch.cuda.synchronize()
+        assert int(flag) == int(one.overflow) == (t == 2)
+        if t != 2:
+            assert abs(float(total) - float(one.sumsq)) <= 64 * 2.0 ** -53 * float(total)
+            assert a.control()["clip_coef"] == one.control()["clip_coef"] < 1.0
+        assert all(torch.equal(x, y) for x, y in zip(p, q))
+        if t == 2:
+            g[0][17] = 0.5
+    assert a.control()["skipped"] == b.control()["skipped"] == 1 and b.control()["t"] == 3
+    with pytest.raises(ValueError, match="dtype"):
+        a.step(norm=(flag.float(), total))
+    with pytest.raises(ValueError, match="dtype"):
+        a.step(norm=(flag, total.float()))
+
+
 @pytest.mark.parametrize("bits8", [False, True])
 def test_empty_list_still_counts_a_step(bits8):
     x = Lists([0, 0], "f32", None, bits8, seed=7)

@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kBlock) tensors_norm_kernel(ListArgs list, dou
         // any inf or NaN among the gradients, or a loss scale without a
         // finite reciprocal, leaves the sum inf or NaN
         const double inv = dyn != nullptr ? 1.0 / dyn->loss_scale : inv_scale;
-        const double total = t * (inv * inv);
+        const double total = t * inv * inv;
         *sumsq = total;
         *overflow = __builtin_isfinite(total) ? 0 : 1;
     }
@@ -839,7 +839,7 @@ int finish_launch() {
 // Workgroups per CU of the long kernels; each was timed against its
 // neighbours on the GPT-2 shaped lists.  Grids that are not a multiple of
 // the CU count lose 10 to 30%.
-//   norm: 5 (1.56e9 bf16 gradients: 443 us; 4: 486, 6: 443, 8: 505)
+//   norm: 5 (1.56e9 bf16 gradients, all streaming: 443 us; 4: 486, 6: 443, 8: 505)
 //   adam, fp32 states: 1 with the next chunk's loads under way (GPT-2 small:
 //     609 us; 2 such: 656, 4 without the loads ahead: 672)
 //   adam, 8-bit states: 3 (a quarter of GPT-2 XL: 1237 us; 2: 1240, 1: 1454)

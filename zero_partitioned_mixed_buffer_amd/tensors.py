@@ -28,6 +28,12 @@ class TensorAdam:
     check_finite (default) takes a pass over the gradients first and skips
     the step if any is inf or NaN; max_grad_norm > 0 (clipping) and
     scale_interval > 0 (dynamic loss scaling, from ``loss_scale``) need it.
+
+    Hyperparameters are ``hp``'s fields and may change between steps, as may
+    ``loss_scale`` (a step captured in a graph keeps those it was captured
+    with).  Lists that share one norm, or ranks that hold parts of the
+    parameters, take it apart from the step: grad_norm() on each, then the
+    sums added and the flags OR-ed, then step(norm=...).
     """
 
     def __init__(self, masters: Sequence, grads: Sequence, params: Optional[Sequence] = None,
@@ -37,7 +43,7 @@ class TensorAdam:
         import torch
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits: {state_bits}, expected 8 or 32")
-        if not masters:
+        if not len(masters):
             raise ValueError("an empty list of tensors")
         if not check_finite and (max_grad_norm > 0 or scale_interval > 0):
             raise ValueError("clipping and dynamic loss scaling need check_finite")
@@ -96,7 +102,7 @@ class TensorAdam:
         # the calls' fixed arguments; every buffer is this object's own
         table = None if self.list.table is None else self.list.table.data_ptr()
         self._head = (self.list.ref, table)
-        self._checks = (self.overflow.data_ptr(), self.sumsq.data_ptr()) if self.check_finite else (None, None)
+        self._checks = (self.overflow.data_ptr(), self.sumsq.data_ptr())
         self._ctl, self._ws = self.ctl.data_ptr(), self.workspace.data_ptr()
 
     def set_grads(self, grads: Sequence):
@@ -113,20 +119,40 @@ class TensorAdam:
                 self.list.table.copy_(new.table)
         self.list.tensors, self.grads = new.tensors, list(grads)
 
-    def step(self, stream=None):
-        """One step on what the gradient tensors hold, scaled by ``loss_scale``
-        (with dynamic scaling by the control block's)."""
+    def grad_norm(self, stream=None):
+        """The gradients' sum of squares (``sumsq``, unscaled) and inf/NaN flag
+        (``overflow``), device tensors of this object; returns both."""
         if B._current_device() != self.device.index:
             import torch
             with torch.cuda.device(self.device):
-                return self.step(stream)
-        s, L, scale = B._stream(stream), B.lib(), self.loss_scale
-        if self.check_finite:
-            dyn = self._ctl if self.hp.scale_interval > 0 else None
-            B._check(L.zero_tensors_grad_norm(*self._head, scale, dyn, *self._checks, self._ws, s),
-                     "zero_tensors_grad_norm")
-        B._check(L.zero_tensors_adam_step(*self._head, C.byref(self.hp), scale, self._ctl, *self._checks,
-                                          B.ROUNDING[self.rounding], self.seed, self._ws, s),
+                return self.grad_norm(stream)
+        dyn = self._ctl if self.hp.scale_interval > 0 else None
+        B._check(B.lib().zero_tensors_grad_norm(*self._head, self.loss_scale, dyn, self.overflow.data_ptr(),
+                                                self.sumsq.data_ptr(), self._ws, B._stream(stream)),
+                 "zero_tensors_grad_norm")
+        return self.overflow, self.sumsq
+
+    def step(self, stream=None, norm=None):
+        """One step on what the gradient tensors hold, scaled by ``loss_scale``
+        (with dynamic scaling by the control block's).  ``norm``: the (flag,
+        sum of squares) device tensors to go by, int32 and float64, where they
+        were taken elsewhere; no pass over the gradients is made then."""
+        if B._current_device() != self.device.index:
+            import torch
+            with torch.cuda.device(self.device):
+                return self.step(stream, norm)
+        if norm is not None:
+            overflow, sumsq = norm
+            B._check_operand(overflow, 1, ("int32",), "overflow flag", self.device.index)
+            B._check_operand(sumsq, 1, ("float64",), "sum of squares", self.device.index)
+            checks = (B._ptr(overflow), B._ptr(sumsq))
+        elif self.check_finite:
+            self.grad_norm(stream)
+            checks = self._checks
+        else:
+            checks = (None, None)
+        B._check(B.lib().zero_tensors_adam_step(*self._head, C.byref(self.hp), self.loss_scale, self._ctl, *checks,
+                                                B.ROUNDING[self.rounding], self.seed, self._ws, B._stream(stream)),
                  "zero_tensors_adam_step")
 
     def control(self) -> dict:
