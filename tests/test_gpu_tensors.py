@@ -664,8 +664,8 @@ def test_other_gradients_and_refusals():
     b.step()
     torch.cuda.synchronize()
     assert torch.equal(pa, pb) and torch.equal(wa, wb)
-    for bad, msg in (([x[:10], x[:10], x[:10]], "expected"), ([g.float() for g in b.grads], "dtype"),
-                     (b.grads[:2], "entries")):
+    for bad, msg in (([x[:10], x[:10], x[:10]], "sizes"), ([g.float() for g in b.grads], "dtype"),
+                     (b.grads[:2], "sizes"), ([None] * 3, "torch tensors")):
         with pytest.raises(ValueError, match=msg):
             b.set_grads(bad)
     assert len(b.grads) == 3 and b.grads[0].numel() == 33

@@ -493,11 +493,43 @@ def _current_device() -> int:
     return torch.cuda.current_device()
 
 
-def _common_dtype(tensors: Sequence, kinds: Tuple[str, ...], what: str) -> str:
-    names = {_dtype_name(t) for t in tensors}
+def _column(tensors: Sequence, numels: Sequence[int], kinds: Tuple[str, ...], what: str,
+            per: int = 1) -> Tuple[str, List[int]]:
+    """Checks a list's tensors of one kind (one dtype, contiguous, one
+    element for ``per`` of the list's) and returns the dtype's name and the
+    addresses."""
+    import torch
+    if len(tensors) != len(numels):
+        raise ValueError(f"{what}: {len(tensors)} entries for {len(numels)} gradients")
+    if not all(isinstance(t, torch.Tensor) for t in tensors):
+        raise ValueError(f"{what}: torch tensors expected")
+    names = {_DTYPE_NAMES.get(d) or str(d).replace("torch.", "") for d in {t.dtype for t in tensors}}
     if len(names) > 1 or not names <= set(kinds):
         raise ValueError(f"{what}: one dtype of {kinds} expected, got {sorted(names)}")
-    return names.pop() if names else kinds[0]
+    for t, n in zip(tensors, numels):
+        if t.numel() != -(-n // per):
+            raise ValueError(f"{what}: {t.numel()} elements where {-(-n // per)} are expected")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: tensors must be contiguous")
+    return names.pop() if names else kinds[0], [t.data_ptr() for t in tensors]
+
+
+def _on_current(columns: Sequence[Sequence]):
+    """Every tensor of the columns is on the current device."""
+    cur = -1
+    for col in columns:
+        for t in col:
+            d = t.get_device()
+            if d != cur or d < 0:
+                _check_current(t, "tensor list")
+                cur = d
+
+
+def _grad_column(grads: Sequence) -> Tuple[int, List[int], List[int]]:
+    import torch
+    numels = [int(t.numel()) if isinstance(t, torch.Tensor) else 0 for t in grads]
+    name, ptrs = _column(grads, numels, tuple(_LIST_TYPES), "gradients")
+    return _LIST_TYPES[name], ptrs, numels
 
 
 class TensorList:
@@ -526,71 +558,58 @@ def tensor_list(grads: Sequence, masters: Optional[Sequence] = None, params: Opt
     and the list holds their addresses: plan again when one moves.
     ``flat_offs`` are the tensors' first random counters (default: packed in
     list order)."""
-    import torch
-    count = len(grads)
-    given = {"masters": masters, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq}
     steps = masters is not None
-    if any((v is not None) != steps for v in given.values()):
+    if any((v is not None) != steps for v in (exp_avg, exp_avg_sq)):
         raise ValueError("masters, exp_avg and exp_avg_sq come together")
     if not steps and (params is not None or avg_scale is not None or sq_scale is not None):
         raise ValueError("a list of gradients alone has no params and no scales")
-    columns = {"grads": grads, "masters": masters, "params": params, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
-               "avg_scale": avg_scale, "sq_scale": sq_scale, "flat_offs": flat_offs}
-    for what, col in columns.items():
-        if col is not None and len(col) != count:
-            raise ValueError(f"{what}: {len(col)} entries for {count} gradients")
-        if col is not None and what != "flat_offs" and not all(isinstance(t, torch.Tensor) for t in col):
-            raise ValueError(f"{what}: torch tensors expected")
-    gtype = _LIST_TYPES[_common_dtype(grads, tuple(_LIST_TYPES), "gradients")]
-    ptype, stype = TYPE_NONE, TYPE_NONE
-    numels = [int(g.numel()) for g in grads]
+    if flat_offs is not None and len(flat_offs) != len(grads):
+        raise ValueError(f"flat_offs: {len(flat_offs)} entries for {len(grads)} gradients")
+    gtype, gptr, numels = _grad_column(grads)
+    ptype = stype = TYPE_NONE
+    columns, keep = {"grad": gptr}, [list(grads)]
     if steps:
-        _common_dtype(masters, ("float32",), "master weights")
+        _, columns["master"] = _column(masters, numels, ("float32",), "masters")
         if params is not None:
-            ptype = _LIST_TYPES[_common_dtype(params, ("float16", "bfloat16"), "params")]
-        kind = _common_dtype([*exp_avg, *exp_avg_sq], ("float32", *_CODES), "states")
+            name, columns["param"] = _column(params, numels, ("float16", "bfloat16"), "params")
+            ptype = _LIST_TYPES[name]
+        kind, columns["exp_avg"] = _column(exp_avg, numels, ("float32", *_CODES), "exp_avg")
         stype = TYPE_F32 if kind == "float32" else TYPE_MX8
+        _, columns["exp_avg_sq"] = _column(exp_avg_sq, numels, (kind,), "exp_avg_sq")
         if (stype == TYPE_MX8) != (avg_scale is not None) or (stype == TYPE_MX8) != (sq_scale is not None):
             raise ValueError("states in 8 bits, and no others, come with avg_scale and sq_scale")
         if stype == TYPE_MX8:
-            _common_dtype([*avg_scale, *sq_scale], _SCALES, "scales")
-    keep = []
-    for what, col in columns.items():
-        if col is None or what == "flat_offs":
-            continue
-        for t, n in zip(col, numels):
-            want = -(-n // MX8_BLOCK) if what.endswith("scale") else n
-            if t.numel() != want:
-                raise ValueError(f"{what}: {t.numel()} elements where {want} are expected")
-            if not t.is_contiguous():
-                raise ValueError(f"{what}: tensors must be contiguous")
-        keep.append(list(col))
-    for col in keep:
-        for t in col:
-            _check_current(t, "tensor list")
-    if flat_offs is None:
-        flat_offs = [0] * count
-        for i in range(1, count):
-            flat_offs[i] = flat_offs[i - 1] + numels[i - 1]
-    arr = (Tensor * max(count, 1))()
-    for i in range(count):
-        t = arr[i]
-        t.n, t.flat_off, t.grad = numels[i], int(flat_offs[i]), _ptr(grads[i])
-        if steps:
-            t.master, t.exp_avg, t.exp_avg_sq = _ptr(masters[i]), _ptr(exp_avg[i]), _ptr(exp_avg_sq[i])
-            if params is not None:
-                t.param = _ptr(params[i])
-            if stype == TYPE_MX8:
-                t.avg_scale, t.sq_scale = _ptr(avg_scale[i]), _ptr(sq_scale[i])
+            _, columns["avg_scale"] = _column(avg_scale, numels, _SCALES, "avg_scale", MX8_BLOCK)
+            _, columns["sq_scale"] = _column(sq_scale, numels, _SCALES, "sq_scale", MX8_BLOCK)
+        keep += [list(c) for c in (masters, params, exp_avg, exp_avg_sq, avg_scale, sq_scale) if c is not None]
+    _on_current(keep)
+    return _plan_list(numels, columns, gtype, ptype, stype, flat_offs, keep)
+
+
+def _plan_list(numels: Sequence[int], columns: dict, gtype: int, ptype: int, stype: int,
+               flat_offs: Optional[Sequence[int]], keep) -> TensorList:
+    """The list of tensors at the addresses in ``columns`` (zero_tensor's
+    fields), its table uploaded to the current device."""
+    import numpy as np
+    import torch
+    count = len(numels)
+    arr = np.zeros((max(count, 1), len(Tensor._fields_)), dtype=np.uint64)
+    at = {name: i for i, (name, _) in enumerate(Tensor._fields_)}
+    if count:
+        arr[:, at["n"]] = numels
+        arr[:, at["flat_off"]] = np.concatenate([[0], np.cumsum(numels[:-1])]) if flat_offs is None else flat_offs
+        for name, ptrs in columns.items():
+            arr[:, at[name]] = ptrs
+    tensors = arr.ctypes.data_as(C.POINTER(Tensor))
     info = TensorListInfo()
-    st = lib().zero_tensors_plan(arr, count, gtype, ptype, stype, C.byref(info), None, 0)
+    st = lib().zero_tensors_plan(tensors, count, gtype, ptype, stype, C.byref(info), None, 0)
     if st not in (ZERO_OK, ZERO_ECAPACITY):
         _check(st, "zero_tensors_plan")
     if info.table_bytes == 0:
         return TensorList(info, None, keep)
     host = torch.empty(int(info.table_bytes) + 16, dtype=torch.uint8)
     host = host[-host.data_ptr() % 16:][:int(info.table_bytes)]
-    _check(lib().zero_tensors_plan(arr, count, gtype, ptype, stype, C.byref(info), host.data_ptr(), host.numel()),
+    _check(lib().zero_tensors_plan(tensors, count, gtype, ptype, stype, C.byref(info), host.data_ptr(), host.numel()),
            "zero_tensors_plan")
     return TensorList(info, host.to(torch.device("cuda", torch.cuda.current_device())), keep)
 

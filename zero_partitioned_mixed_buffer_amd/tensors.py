@@ -85,17 +85,28 @@ class TensorAdam:
         self.seed = int(seed) & (2**64 - 1)
         self._plan()
 
-    def _views(self, flat, per=1):
-        return [flat[o // per:o // per + -(-n // per)] for o, n in zip(self.state_offs, self.numels)]
-
     def _tensor_list(self, grads):
         import torch
         mx = self.state_bits == 8
         with torch.cuda.device(self.device):
-            return B.tensor_list(grads, self.masters, self.params, self._views(self.exp_avg),
-                                 self._views(self.exp_avg_sq),
-                                 self._views(self.avg_scale, B.MX8_BLOCK) if mx else None,
-                                 self._views(self.sq_scale, B.MX8_BLOCK) if mx else None, self.flat_offs)
+            gtype, ptrs, numels = B._grad_column(grads)
+            if numels != self.numels:
+                raise ValueError("gradients: the sizes of the master weights expected")
+            columns = {"grad": ptrs, "master": B._column(self.masters, numels, ("float32",), "masters")[1]}
+            ptype, keep = B.TYPE_NONE, [grads, self.masters, self.exp_avg, self.exp_avg_sq]
+            if self.params is not None:
+                name, columns["param"] = B._column(self.params, numels, ("float16", "bfloat16"), "params")
+                ptype = B._LIST_TYPES[name]
+                keep.append(self.params)
+            B._on_current([grads, self.masters, self.params or ()])
+            for name, flat, per in (("exp_avg", self.exp_avg, 1), ("exp_avg_sq", self.exp_avg_sq, 1),
+                                    ("avg_scale", self.avg_scale, B.MX8_BLOCK),
+                                    ("sq_scale", self.sq_scale, B.MX8_BLOCK)):
+                if flat is not None:
+                    base, size = flat.data_ptr(), flat.element_size()
+                    columns[name] = [base + o // per * size for o in self.state_offs]
+                    keep.append(flat)
+            return B._plan_list(numels, columns, gtype, ptype, B.TYPE_MX8 if mx else B.TYPE_F32, self.flat_offs, keep)
 
     def _plan(self):
         self.list = self._tensor_list(self.grads)
@@ -111,13 +122,14 @@ class TensorAdam:
         have ended).  The list's table is rewritten in place, so that steps
         captured in a graph read the new tensors too."""
         import torch
-        new = self._tensor_list(list(grads))
+        grads = list(grads)
+        new = self._tensor_list(grads)
         if new.info.grad_type != self.list.info.grad_type:
             raise ValueError(f"gradients: dtype {grads[0].dtype}, but the list was planned with {self.grads[0].dtype}")
         with torch.cuda.device(self.device):
             if new.table is not None:
                 self.list.table.copy_(new.table)
-        self.list.tensors, self.grads = new.tensors, list(grads)
+        self.list.tensors, self.grads = new.tensors, grads
 
     def grad_norm(self, stream=None):
         """The gradients' sum of squares (``sumsq``, unscaled) and inf/NaN flag
