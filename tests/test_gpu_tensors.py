@@ -537,6 +537,42 @@ def test_empty_list_still_counts_a_step(bits8):
     assert x.step(check=False)["t"] == 2
 
 
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_in_a_training_loop(state_bits):
+    """Autograd's gradients, accumulated into the tensors that the list was
+    planned with, through norm, clipped step and 16-bit copy; the oracle
+    steps on the same gradients."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam
+    torch.manual_seed(1)
+    net = torch.nn.Sequential(torch.nn.Linear(33, 70), torch.nn.Tanh(), torch.nn.Linear(70, 5)).cuda()
+    params = list(net.parameters())
+    for p in params:
+        p.grad = torch.zeros_like(p)
+    copies = [p.detach().bfloat16() for p in params]
+    hp = dict(lr=3e-3, weight_decay=0.1)
+    opt = TensorAdam(params, [p.grad for p in params], copies, state_bits=state_bits, max_grad_norm=0.5, seed=21, **hp)
+    ref = to.TensorAdam([p.detach().cpu().numpy().reshape(-1) for p in params], state_bits, seed=21, **hp)
+    for t in range(6):
+        net.zero_grad(set_to_none=False)
+        net(torch.randn(64, 33, device="cuda")).square().mean().backward()
+        opt.step()
+        torch.cuda.synchronize()
+        ctl = opt.control()
+        ref.step([p.grad.cpu().numpy().reshape(-1) for p in params], coef=ctl["clip_coef"])
+        assert ctl["t"] == t + 1 and ctl["clip_coef"] <= 1.0
+        for i, (p, w) in enumerate(zip(params, copies)):
+            o, n = opt.state_offs[i], p.numel()
+            if state_bits == 32:
+                assert np.array_equal(bits(p.detach()).reshape(-1), ref.p[i].view(np.uint32)), (t, i)
+                assert np.array_equal(bits(opt.exp_avg[o:o + n]), ref.m[i].view(np.uint32))
+                assert np.array_equal(bits(opt.exp_avg_sq[o:o + n]), ref.v[i].view(np.uint32))
+            else:  # the weights' bound is tested above; they meet the states through the gradients alone
+                assert np.array_equal(bits(opt.exp_avg[o:o + n]), ref.m[i][0])
+                assert np.array_equal(bits(opt.exp_avg_sq[o:o + n]), ref.v[i][0])
+            assert torch.equal(w, p.detach().bfloat16())
+
+
 # ------------------------------------------------------------ graphs, streams
 def _adam_pair(state_bits, n=70001, **kw):
     torch = torch_mod()

@@ -593,7 +593,7 @@ def _plan_list(numels: Sequence[int], columns: dict, gtype: int, ptype: int, sty
     import numpy as np
     import torch
     count = len(numels)
-    arr = np.zeros((max(count, 1), len(Tensor._fields_)), dtype=np.uint64)
+    arr = np.zeros((max(count, 1), len(Tensor._fields_)), dtype=np.int64)
     at = {name: i for i, (name, _) in enumerate(Tensor._fields_)}
     if count:
         arr[:, at["n"]] = numels

@@ -113,7 +113,7 @@ __device__ __forceinline__ uint32_t max8(uint32_t x) {
 // Draws a ticket for the workgroup (one thread of it): true for the last of
 // the grid, which leaves the counters at zero.  Draws on one address follow
 // each other at about 10 ns, so the workgroups draw from 32 counters, and
-// the last of each draws from the one behind them (600 workgroups: 16.0 us
+// the last of each draws from the one behind them (600 workgroups: 15.9 us
 // of kernel on one counter, 12.5 on 33).  The order is relaxed: what has
 // to be seen by the last workgroup has to be performed before the draw.
 __device__ __forceinline__ bool last_to_draw(uint32_t* ticket) {
@@ -873,9 +873,10 @@ int finish_launch() {
 constexpr int kNormPerCu = 5;
 constexpr int kAdamPerCu = 1;
 constexpr int kAdamMxPerCu = 3;
-// fp32 states: a list of at most this many chunks per CU takes one workgroup
-// a chunk, all in flight at once (400 tensors, 600 chunks: 14.3 us; 17.1
-// on kAdamPerCu).
+// fp32 states: a list of at most kAdamShortChunks chunks per CU takes more
+// workgroups without loads ahead (400 tensors, 600 chunks: 14.3 us; 17.1 on
+// kAdamPerCu; 2048 chunks: 44.0 and 46.0; 4096: 85.0 and 83.1).
+constexpr int kAdamShortChunks = 8;
 constexpr int kAdamShortPerCu = 4;
 // A list of more than twice this many chunks is stepped in launches of
 // about 2^26 elements (a quarter of GPT-2 XL, one launch against six: 1951
@@ -910,7 +911,7 @@ int adam_with(const ListArgs& list, const TensorStepArgs& a, hipStream_t s) {
         return a.stochastic ? adam_launches<kGrad, kParam, true, true, true>(list, a, grid, s)
                             : adam_launches<kGrad, kParam, true, false, true>(list, a, grid, s);
     }
-    if (list.n_chunks <= static_cast<int64_t>(cu_count()) * kAdamShortPerCu)
+    if (list.n_chunks <= static_cast<int64_t>(cu_count()) * kAdamShortChunks)
         return adam_launches<kGrad, kParam, false, false, false>(list, a, grid_of(list.n_chunks, kAdamShortPerCu), s);
     return adam_launches<kGrad, kParam, false, false, true>(list, a, grid_of(list.n_chunks, kAdamPerCu), s);
 }
