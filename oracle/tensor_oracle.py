@@ -59,13 +59,13 @@ def code_values() -> np.ndarray:
     return np.where(c & 0x80, -v, v)
 
 
-def mx8_encode(x, root: bool = False, words=None):
+def mx8_encode(x, root: bool = False, words=None, taken: bool = False):
     """float32 array -> (codes uint8[n], scale bytes uint8[ceil(n/32)]); words
-    None rounds to nearest."""
+    None rounds to nearest.  taken: x are the roots themselves."""
     x = np.asarray(x, dtype=F32)
     n = x.size
     with np.errstate(invalid="ignore"):
-        x = np.sqrt(x) if root else x
+        x = np.sqrt(x) if root and not taken else x
     pad = -n % 32
     b = np.concatenate([x, np.zeros(pad, F32)]).reshape(-1, 32).astype(F64)
     bad = ~np.isfinite(b).all(axis=1)
@@ -140,19 +140,26 @@ class TensorAdam:
     def _enc(self, x, root, words):
         return mx8_encode(x, root, words) if self.bits == 8 else x
 
-    def _dec(self, s, root):
-        return mx8_decode(*s, root=root) if self.bits == 8 else s
+    def _step8(self, i, g, sc, words):
+        """In float64 throughout, rounded to fp32 at the end; the root of a
+        variance past fp32's range is that of the float64 value."""
+        m = mx8_decode(*self.m[i]).astype(F64)
+        v = mx8_decode(*self.v[i]).astype(F64) ** 2
+        p, m, v = zo.adam_update(self.p[i].astype(F64), m, v, g, sc)
+        r = np.sqrt(v.astype(F32))
+        past = np.isinf(r)
+        r[past] = np.sqrt(v[past]).astype(F32)
+        return p.astype(F32), mx8_encode(m.astype(F32), False, words), mx8_encode(r, True, words, taken=True)
 
     def step(self, grads, loss_scale=1.0, coef=1.0):
         sc = zo.step_scalars(*self.hp, self.b1p, self.b2p)
         factor = coef * (1.0 / loss_scale)
         with np.errstate(all="ignore"):
             for i, g in enumerate(grads):
-                n = self.p[i].size
-                p, m, v = zo.adam_update(self.p[i], self._dec(self.m[i], False), self._dec(self.v[i], True),
-                                         raw_grad(g).reshape(-1) * factor, sc)
-                w = None
-                if self.bits == 8 and self.stochastic:
-                    w = random_words(n, self.seed, self.t + 1, int(self.offs[i]))
-                self.p[i], self.m[i], self.v[i] = p, self._enc(m, False, w), self._enc(v, True, w)
+                g = raw_grad(g).reshape(-1) * factor
+                if self.bits == 32:
+                    self.p[i], self.m[i], self.v[i] = zo.adam_update(self.p[i], self.m[i], self.v[i], g, sc)
+                    continue
+                w = random_words(g.size, self.seed, self.t + 1, int(self.offs[i])) if self.stochastic else None
+                self.p[i], self.m[i], self.v[i] = self._step8(i, g, sc, w)
         self.t, self.b1p, self.b2p = self.t + 1, sc["b1t"], sc["b2t"]

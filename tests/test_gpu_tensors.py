@@ -418,6 +418,21 @@ def test_unchecked_inf_stays_in_its_block():
         assert x.arena.gaps_intact()
 
 
+def test_huge_gradient_stays_finite():
+    """A finite gradient whose square passes fp32's range is no overflow: 8-bit
+    states hold the root of its variance, and no weight or state turns inf
+    or NaN."""
+    x = Lists([40, 4097], "f32", None, True, seed=16)
+    x.step()
+    assert x.step(poison=(1, 70, 1e25))["overflow"] == 0
+    x.check()
+    for t in range(3):
+        x.step()
+        x.check(t)
+    assert bits(x.ms[1])[2] != 255 and bits(x.vs[1])[2] != 255
+    assert all(bool(p.isfinite().all()) for p in x.p)
+
+
 def test_shared_gradient():
     """One gradient tensor for two weights (a tied pair held twice)."""
     torch = torch_mod()

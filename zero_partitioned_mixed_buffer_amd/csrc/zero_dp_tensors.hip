@@ -205,6 +205,27 @@ __device__ __forceinline__ void roots4(fvec& x) {
     }
 }
 
+// Roots of the variances v, given in float64: those of their fp32 values, and
+// past fp32's range those of v itself, whose roots fp32 still holds (one
+// huge gradient would else turn its block, and 32 weights, into NaN).
+__device__ __forceinline__ fvec wide_roots4(const double (&v)[kV]) {
+    fvec x;
+    uint32_t most = 0;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) {
+        x[e] = static_cast<float>(v[e]);
+        most = max(most, bits_of(x[e]));
+    }
+    if (__any(most >= 0x7F800000u)) {
+#pragma unroll
+        for (int e = 0; e < kV; ++e)
+            x[e] = bits_of(x[e]) >= 0x7F800000u ? static_cast<float>(__builtin_sqrt(v[e])) : __builtin_sqrtf(x[e]);
+        return x;
+    }
+    roots4(x);
+    return x;
+}
+
 // The four codes of x under their block's scale byte.  The conversions take
 // the scale as an operand.  Their stochastic form adds the top 20 bits of
 // its random operand to the mantissa's last 20 bits and cuts them off,
@@ -227,36 +248,24 @@ __device__ __forceinline__ uint32_t codes4(const fvec& x, float scale, const uin
 }
 
 // Encodes a lane's four elements of a block (8 lanes, all of them here, with
-// zeros for elements that are not).  kRoot: x >= 0 are variances, encoded by
-// their square roots, which replace them.
+// zeros for elements that are not).  kRoot: x are roots.
 template <bool kRoot, bool kStoch>
-__device__ __forceinline__ uint32_t encode4(fvec& x, const uint32_t (&word)[kV], uint32_t& byte) {
-    uint32_t big;
+__device__ __forceinline__ uint32_t encode4(const fvec& x, const uint32_t (&word)[kV], uint32_t& byte) {
+    uint32_t big = 0;
     uint32_t bits[kV];
-    fvec y;
+    fvec y = x;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) {
+        big = max(big, bits_of(x[e]) & 0x7FFFFFFFu);
+        bits[e] = kRoot ? word[e] << 16 : word[e];
+    }
+    byte = scale_byte(max8(big));
     if (kRoot) {
-        const fvec v = x;
-        roots4(x);
-        big = max8(max(max(bits_of(x[0]), bits_of(x[1])), max(bits_of(x[2]), bits_of(x[3]))) & 0x7FFFFFFFu);
-        byte = scale_byte(big);
         // a positive root keeps at least the smallest code: rounded to zero
         // it would turn its weight's next update into m/eps
         const float least = __builtin_bit_cast(float, byte << 23) * 0x1p-9f;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            y[e] = v[e] > 0.0f ? __builtin_fmaxf(x[e], least) : static_cast<float>(x[e]);
-            bits[e] = word[e] << 16;
-        }
-    } else {
-        big = 0;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            big = max(big, bits_of(x[e]) & 0x7FFFFFFFu);
-            bits[e] = word[e];
-            y[e] = x[e];
-        }
-        big = max8(big);
-        byte = scale_byte(big);
+        for (int e = 0; e < kV; ++e) y[e] = x[e] > 0.0f ? __builtin_fmaxf(x[e], least) : static_cast<float>(x[e]);
     }
     const uint32_t c = codes4<kStoch>(y, __builtin_bit_cast(float, byte << 23), bits);
     return byte == 255u ? 0x7F7F7F7Fu : c;
@@ -635,16 +644,17 @@ struct Row {
         uint32_t m4 = 0, v4 = 0;
         if (kMx) {
             m = decode4(mc, scale_value(mb));
-            v = decode4(vc, scale_value(vb));
-            v = v * v;
+            v = decode4(vc, scale_value(vb));  // roots: four significant bits, so their squares are exact
+            double v1[kV];
 #pragma unroll
             for (int e = 0; e < kV; ++e) {
                 const double g1 = g.at(e) * c.factor;
                 const double m1 = (c.b1 * static_cast<double>(m[e])) + (c.omb1 * g1);
-                const double v1 = (c.b2 * static_cast<double>(v[e])) + (c.omb2 * (g1 * g1));
+                const double r = static_cast<double>(v[e]);
+                v1[e] = (c.b2 * (r * r)) + (c.omb2 * (g1 * g1));
                 mo[e] = static_cast<float>(m1);
-                vo[e] = static_cast<float>(v1);
             }
+            vo = wide_roots4(v1);
             uint32_t word[kV] = {0, 0, 0, 0};
             if (kStoch) {
 #pragma unroll
@@ -652,7 +662,7 @@ struct Row {
             }
             uint32_t mbyte, vbyte;
             m4 = encode4<false, kStoch>(mo, word, mbyte);
-            v4 = encode4<true, kStoch>(vo, word, vbyte);  // vo: now the roots
+            v4 = encode4<true, kStoch>(vo, word, vbyte);
             if ((threadIdx.x & 7) == 0 && (kFull || j < k.n)) {
                 k.ms[j / zdp::kMxBlock] = static_cast<uint8_t>(mbyte);
                 k.vs[j / zdp::kMxBlock] = static_cast<uint8_t>(vbyte);
@@ -801,6 +811,7 @@ __global__ void __launch_bounds__(kBlock) mx8_encode_kernel(const float* x_in, i
                 for (int e = 0; e < kV; ++e)
                     word[e] = random_word(key, counter + static_cast<uint32_t>(base) + static_cast<uint32_t>(j + e));
             }
+            if (kRoot) roots4(v[u]);
             uint32_t byte;
             const uint32_t c = encode4<kRoot, kStoch>(v[u], word, byte);
             if (j + kV <= rest)
