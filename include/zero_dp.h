@@ -563,9 +563,9 @@ int zero_tensors_grad_norm(const zero_tensor_list* list, const void* table, doub
  * fp32, then m' and r = fp32(sqrt(v')) (of the unrounded v' past fp32's range)
  * encoded as zero_mx8_encode does, and the update in fp32 arithmetic, p' =
  * p - (lr wd p + lr/(1-b1^t) m' / (r / sqrt(1-b2^t) + eps)), eps not below
- * 2^-126 (off by at most 12 * 2^-24 of the update's terms and the rounding of p').  The step number and the beta powers are ctl's; the
- * last launch's last workgroup commits the step there (t += 1; `cur` is not
- * used).
+ * 2^-126 (off by at most 12 * 2^-24 of the update's terms, and p' rounded).
+ * The step number and the beta powers are ctl's; the last launch's last
+ * workgroup commits the step there (t += 1; `cur` is not used).
  *   ctl: belongs to one list, since every step of the list advances it; lists
  *     stepped under one norm have a control block each.
  *   overflow: device flag of zero_tensors_grad_norm; nonzero skips the step:
@@ -589,8 +589,8 @@ int zero_tensors_adam_step(const zero_tensor_list* list, const void* table, cons
  * first (a variance; a negative x makes its block NaN) and decode squares.
  * step, flat_off: of the random words (ZERO_ROUND_STOCHASTIC).  Encoding is
  * what a step does with its new state, bit for bit.  Decode takes any scale
- * byte (0 is 2^-127, 255 NaN); a square past fp32's range is inf.  x: device, 4-byte aligned; no two of the
- * arrays may overlap.
+ * byte (0 is 2^-127, 255 NaN); a square past fp32's range is inf.
+ *   x: device, 4-byte aligned; no two of the arrays may overlap.
  * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW, ZERO_EALIAS, ZERO_EHIP.
  */
 int zero_mx8_encode(const float* x, int64_t n, int32_t root, uint8_t* codes, uint8_t* scales, int32_t rounding,

@@ -643,6 +643,36 @@ def test_graph_replays_match_eager_steps(state_bits):
     assert eager[0].control()["skipped"] == 2
 
 
+def test_graphs_share_a_workspace():
+    """Two captured lists on one workspace, replayed in turn on one stream
+    with eager work between: every call leaves it ready for the next."""
+    torch = torch_mod()
+    pairs = [_adam_pair(8, n=9001, seed=2, max_grad_norm=0.1), _adam_pair(32, n=300007, max_grad_norm=0.1)]
+    graphs = []
+    for eager, graphed in pairs:
+        graphed[0].workspace = pairs[0][1][0].workspace
+        graphed[0]._plan()
+        for o in (eager, graphed):
+            o[0].step()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            graphed[0].step()
+    for rep in range(4):
+        for (eager, graphed), graph in zip(pairs, graphs):
+            x = (torch.randn(eager[2].shape, device="cuda") * 1e-3).bfloat16()
+            if rep == 1:
+                x[7] = float("nan")
+            eager[2].copy_(x)
+            graphed[2].copy_(x)
+            graph.replay()
+            eager[0].step()
+    torch.cuda.synchronize()
+    for eager, graphed in pairs:
+        _same(eager, graphed)
+        assert eager[0].control()["skipped"] == 1 and eager[0].control()["t"] == 4
+
+
 def test_graph_sees_other_gradients():
     """A captured step reads the tensors that set_grads named since."""
     torch = torch_mod()
