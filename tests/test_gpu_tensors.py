@@ -754,6 +754,10 @@ def test_other_gradients_and_refusals():
         TensorAdam([pa, pa], [x, x])  # the same weight twice
     with pytest.raises(B.ZeroError):
         TensorAdam([pa[:100], pa[99:200]], [x[:100], x[99:200]])
+    with pytest.raises(ValueError, match="flat_offs"):
+        TensorAdam([pa[:100], pa[100:200]], [x[:100], x[100:200]], flat_offs=[0])
+    with pytest.raises(B.ZeroError):
+        TensorAdam([pa], [x], flat_offs=[-1])
 
 
 # ----------------------------------------------------------------- checkpoint

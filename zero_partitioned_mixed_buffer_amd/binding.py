@@ -563,8 +563,6 @@ def tensor_list(grads: Sequence, masters: Optional[Sequence] = None, params: Opt
         raise ValueError("masters, exp_avg and exp_avg_sq come together")
     if not steps and (params is not None or avg_scale is not None or sq_scale is not None):
         raise ValueError("a list of gradients alone has no params and no scales")
-    if flat_offs is not None and len(flat_offs) != len(grads):
-        raise ValueError(f"flat_offs: {len(flat_offs)} entries for {len(grads)} gradients")
     gtype, gptr, numels = _grad_column(grads)
     ptype = stype = TYPE_NONE
     columns, keep = {"grad": gptr}, [list(grads)]
@@ -593,6 +591,8 @@ def _plan_list(numels: Sequence[int], columns: dict, gtype: int, ptype: int, sty
     import numpy as np
     import torch
     count = len(numels)
+    if flat_offs is not None and len(flat_offs) != count:
+        raise ValueError(f"flat_offs: {len(flat_offs)} entries for {count} gradients")
     arr = np.zeros((max(count, 1), len(Tensor._fields_)), dtype=np.int64)
     at = {name: i for i, (name, _) in enumerate(Tensor._fields_)}
     if count:
