@@ -563,7 +563,8 @@ int zero_tensors_grad_norm(const zero_tensor_list* list, const void* table, doub
  * fp32, then m' and r = fp32(sqrt(v')) (of the unrounded v' past fp32's range)
  * encoded as zero_mx8_encode does, and the update in fp32 arithmetic, p' =
  * p - (lr wd p + lr/(1-b1^t) m' / (r / sqrt(1-b2^t) + eps)), eps not below
- * 2^-126 (off by at most 12 * 2^-24 of the update's terms, and p' rounded).
+ * 2^-126 (off by at most 12 * 2^-24 of the update's terms, and p' rounded;
+ * an element whose denominator passes 2^125 is updated in float64).
  * The step number and the beta powers are ctl's; the last launch's last
  * workgroup commits the step there (t += 1; `cur` is not used).
  *   ctl: belongs to one list, since every step of the list advances it; lists

@@ -208,7 +208,8 @@ __device__ __forceinline__ void roots4(fvec& x) {
 // Roots of the variances v, given in float64: those of their fp32 values, and
 // past fp32's range those of v itself, whose roots fp32 still holds (one
 // huge gradient would else turn its block, and 32 weights, into NaN).
-__device__ __forceinline__ fvec wide_roots4(const double (&v)[kV]) {
+// wide: some lane of the wave holds such a variance.
+__device__ __forceinline__ fvec wide_roots4(const double (&v)[kV], bool& wide) {
     fvec x;
     uint32_t most = 0;
 #pragma unroll
@@ -216,7 +217,8 @@ __device__ __forceinline__ fvec wide_roots4(const double (&v)[kV]) {
         x[e] = static_cast<float>(v[e]);
         most = max(most, bits_of(x[e]));
     }
-    if (__any(most >= 0x7F800000u)) {
+    wide = __any(most >= 0x7F800000u);
+    if (wide) {
 #pragma unroll
         for (int e = 0; e < kV; ++e)
             x[e] = bits_of(x[e]) >= 0x7F800000u ? static_cast<float>(__builtin_sqrt(v[e])) : __builtin_sqrtf(x[e]);
@@ -654,7 +656,8 @@ struct Row {
                 v1[e] = (c.b2 * (r * r)) + (c.omb2 * (g1 * g1));
                 mo[e] = static_cast<float>(m1);
             }
-            vo = wide_roots4(v1);
+            bool wide;
+            vo = wide_roots4(v1, wide);
             uint32_t word[kV] = {0, 0, 0, 0};
             if (kStoch) {
 #pragma unroll
@@ -671,6 +674,18 @@ struct Row {
             for (int e = 0; e < kV; ++e) {
                 const float q = mo[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(vo[e], c.isbf, c.epsf));
                 po[e] = p[e] - __builtin_fmaf(c.lrwdf, p[e], c.ssf * q);
+            }
+            // The hardware's reciprocal has no denormal results: above 2^126
+            // it is 0 and the weight would stay.  1/sqrt(1-b2^t) <= 2^26.5,
+            // so such a denominator has a root above 2^98, whose variance is
+            // past fp32's range, or a huge eps.  Its element takes float64.
+            if (wide || c.epsf >= 0x1p124f) {
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    if (!(__builtin_fmaf(vo[e], c.isbf, c.epsf) >= 0x1p125f)) continue;
+                    const double q = static_cast<double>(mo[e]) / (static_cast<double>(vo[e]) * c.isb + c.eps);
+                    po[e] = static_cast<float>((static_cast<double>(p[e]) * c.dcy) - (c.ss * q));
+                }
             }
         } else {
 #pragma unroll
