@@ -470,6 +470,8 @@ int zero_gather_layers(const uint16_t* const* windows, int32_t nd, int64_t part,
  * for 2^(e - 127), and each element is one e4m3 code (OCP FP8: 4 exponent
  * bits, 3 mantissa bits, largest finite value 448).  An encoded block has
  * the smallest e >= 1 that keeps its largest magnitude within 448 scales;
+ * at the largest such scale, 2^120, a magnitude past 240 scales keeps 240
+ * (the next code, 256, would read as inf);
  * a block that holds an inf or a NaN has e = 255 and every code NaN.  A
  * positive root keeps at least the smallest positive code, since a root of
  * 0 would turn the next update into m / eps.

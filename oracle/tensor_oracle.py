@@ -13,6 +13,7 @@ definition, in powers and floors on float64:
 * an element is y = |x| / scale rounded to e4m3: steps of 2^(k - 3) for
   2^k <= y < 2^(k + 1), and of 2^-9 below 2^-6; nearest with ties to even, or
   floor(y / step + R / 2^20) steps with 20 random bits R;
+* at the scale 2^120 y is at most 240 (256 * 2^120 would be inf in fp32);
 * a root is fp32(sqrt(x)), and one that is positive keeps y >= 2^-9.
 """
 from __future__ import annotations
@@ -80,6 +81,7 @@ def mx8_encode(x, root: bool = False, words=None, taken: bool = False):
     y = np.abs(np.where(bad[:, None], 0.0, b)) / 2.0 ** (e - 127.0)[:, None]
     if root:
         y = np.where(b > 0, np.maximum(y, 2.0 ** -9), y)
+    y = np.where((e == 247)[:, None], np.minimum(y, 240.0), y)  # 256 * 2^120 is no float32
     step = 2.0 ** (np.floor(np.log2(np.maximum(y, 2.0 ** -6))) - 3)
     if words is None:
         y = np.round(y / step) * step  # ties to even

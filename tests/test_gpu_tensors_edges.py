@@ -2,11 +2,17 @@
 calls that the parity tests do not make: against the oracle where it applies,
 with the bounds derived at the head of test_gpu_tensors.py.
 """
+import numpy as np
 import pytest
 
-from test_gpu_tensors import Lists
+from oracle import tensor_oracle as to
+
+from gpu_util import torch_mod
+from test_gpu_tensors import Lists, bits
 
 pytestmark = pytest.mark.gpu
+
+F32 = np.float32
 
 
 # ------------------------------------------------------------ top of the range
@@ -31,3 +37,33 @@ def test_eps_past_the_range(eps):
     for t in range(3):
         x.step(poison=(1, 70, 3e38))
         x.check(t)
+
+
+@pytest.mark.parametrize("beta1,beta2", [(0.9, 0.5), (0.0, 0.999), (0.9, 0.0)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_largest_gradients_leave_finite_states(kind, beta1, beta2):
+    """A finite gradient next to the largest float again and again: no state
+    may round to 2^128, which would read as inf and turn 32 weights into NaN."""
+    x = Lists([40, 4097], kind, None, True, seed=33, beta1=beta1, beta2=beta2)
+    for t in range(10):
+        x.step(poison=(1, 70, 3.38e38))
+        x.check(t)
+    assert all(bool(p.isfinite().all()) for p in x.p)
+
+
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+def test_encode_of_the_largest_floats_decodes_finite(rounding):
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import mx8_decode, mx8_encode
+    top = 240 * 2.0 ** 120
+    vals = np.array([np.finfo(F32).max, -np.finfo(F32).max, 3.2e38, top, -top, 3.1e38, 1e38, 0.0] * 4, dtype=F32)
+    x = torch.from_numpy(vals).cuda()
+    c, s = torch.zeros(32, dtype=torch.uint8, device="cuda"), torch.zeros(1, dtype=torch.uint8, device="cuda")
+    back = torch.empty(32, device="cuda")
+    mx8_encode(x, c, s, rounding=rounding, seed=5)
+    mx8_decode(c, s, back)
+    want = to.mx8_encode(vals, words=to.random_words(32, 5, 0) if rounding == "stochastic" else None)
+    assert np.array_equal(bits(c), want[0]) and int(s) == want[1][0] == 247
+    got = back.cpu().numpy()
+    assert np.array_equal(got[:5], np.array([top, -top, top, top, -top], dtype=F32))
+    assert np.isfinite(got).all() and (np.abs(got - vals)[5:8] <= 2.0 ** 124).all()  # one step of e4m3

@@ -18,7 +18,8 @@
 //   encode   blocks of 32 fp32 values: scale 2^(e-127) with the smallest e >= 1
 //            that keeps the largest magnitude within 448 scales, each value
 //            over the scale in e4m3 (nearest, or stochastic: the random word's
-//            top 20 bits added to the 20 bits that are cut off)
+//            top 20 bits added to the 20 bits that are cut off), at most
+//            240 at scale 2^120
 //   decode   value = code * scale, squared for a root
 //
 // Everything here is a stream over memory.  No two workgroups write the same
@@ -255,19 +256,24 @@ template <bool kRoot, bool kStoch>
 __device__ __forceinline__ uint32_t encode4(const fvec& x, const uint32_t (&word)[kV], uint32_t& byte) {
     uint32_t big = 0;
     uint32_t bits[kV];
-    fvec y = x;
 #pragma unroll
     for (int e = 0; e < kV; ++e) {
         big = max(big, bits_of(x[e]) & 0x7FFFFFFFu);
         bits[e] = kRoot ? word[e] << 16 : word[e];
     }
     byte = scale_byte(max8(big));
-    if (kRoot) {
-        // a positive root keeps at least the smallest code: rounded to zero
-        // it would turn its weight's next update into m/eps
-        const float least = __builtin_bit_cast(float, byte << 23) * 0x1p-9f;
+    // the largest scale's codes end at 240: 256 * 2^120 would read as inf
+    constexpr float most = 0x1.Ep127f;
+    // a positive root keeps at least the smallest code: rounded to zero it
+    // would turn its weight's next update into m/eps
+    const float least = __builtin_bit_cast(float, byte << 23) * 0x1p-9f;
+    fvec y;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) y[e] = x[e] > 0.0f ? __builtin_fmaxf(x[e], least) : static_cast<float>(x[e]);
+    for (int e = 0; e < kV; ++e) {
+        if (kRoot)
+            y[e] = x[e] > 0.0f ? __builtin_amdgcn_fmed3f(x[e], least, most) : static_cast<float>(x[e]);
+        else
+            y[e] = __builtin_amdgcn_fmed3f(x[e], -most, most);
     }
     const uint32_t c = codes4<kStoch>(y, __builtin_bit_cast(float, byte << 23), bits);
     return byte == 255u ? 0x7F7F7F7Fu : c;
