@@ -8,7 +8,7 @@ import pytest
 from oracle import tensor_oracle as to
 
 from gpu_util import torch_mod
-from test_gpu_tensors import Lists, bits
+from test_gpu_tensors import Lists, _adam_pair, bits
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +67,38 @@ def test_encode_of_the_largest_floats_decodes_finite(rounding):
     got = back.cpu().numpy()
     assert np.array_equal(got[:5], np.array([top, -top, top, top, -top], dtype=F32))
     assert np.isfinite(got).all() and (np.abs(got - vals)[5:8] <= 2.0 ** 124).all()  # one step of e4m3
+
+
+# ----------------------------------------------------------------- checkpoints
+@pytest.mark.parametrize("src,dst", [(32, 8), (8, 32)])
+def test_variance_past_the_range_between_widths(src, dst):
+    """A 1e25 gradient leaves a 32-bit list with v = inf and an 8-bit one with
+    a root that no 32-bit variance holds; both go on in the other width, and
+    the weight moves by less than lr a step: |m| / r is cut to 1, or kept at
+    0.1 / sqrt(0.001) = 3.16 (each off by a code, 1/8), and multiplied by 0.9
+    sqrt(1-b2^t) / (1-b1^t) < 0.2 at steps 3 and 4."""
+    torch = torch_mod()
+    a, b = _adam_pair(src)[0], _adam_pair(dst)[0]
+    a[2].normal_(0, 1e-3)
+    a[0].step()
+    a[2][6000] = 1e25
+    a[0].step()
+    assert a[0].control()["overflow"] == 0 and bool(a[1].isfinite().all())
+    b[0].load_state_dict(a[0].state_dict())
+    at = b[0].state_offs[2] + 6000 - 5000
+    if dst == 32:
+        assert float(b[0].exp_avg_sq[at]) == np.finfo(F32).max
+        assert bool(b[0].exp_avg.isfinite().all()) and bool(b[0].exp_avg_sq.isfinite().all())
+        ratio = float(b[0].exp_avg[at]) / 2.0 ** 64
+        assert abs(ratio / (0.1 / 0.001 ** 0.5) - 1) < 0.27  # 9/8 over 8/9
+    else:
+        assert int((bits(b[0].sq_scale) == 255).sum()) == 0 and int((bits(b[0].avg_scale) == 255).sum()) == 0
+    before = b[1].clone()
+    b[2].normal_(0, 1e-3)
+    b[0].step()
+    one = b[1].clone()
+    b[0].step()
+    torch.cuda.synchronize()
+    assert bool(b[1].isfinite().all())
+    assert 0 < float((one - before)[6000].abs()) < 1e-3 and 0 < float((b[1] - one)[6000].abs()) < 1e-3
+    assert float((b[1] - before).abs().max()) < 2e-2

@@ -208,7 +208,11 @@ class TensorAdam:
     def load_state_dict(self, sd: dict):
         """Restores a state_dict of a list of the same sizes.  Of the same
         state_bits it resumes exactly; states of the other width are encoded
-        (to nearest) or decoded.  The 16-bit copies are written anew."""
+        (to nearest) or decoded.  A variance that float32 does not hold (a
+        gradient above 1e19 was met) is then taken as its largest value and
+        its momentum cut with it, so that the weight's next updates keep
+        their size, or stay below lr where that size is lost too (an infinite
+        32-bit variance).  The 16-bit copies are written anew."""
         import numpy as np
         import torch
         if [int(x) for x in np.asarray(sd["numels"])] != self.numels:
@@ -235,6 +239,8 @@ class TensorAdam:
                 if self.params is not None:
                     self.params[i].detach().copy_(m.detach())
                 at += n
+            if not mx and self.state_bits == 8:
+                self._cut_variances(arr["exp_avg"], arr["exp_avg_sq"])
             for k, scale, root in (("exp_avg", "avg_scale", False), ("exp_avg_sq", "sq_scale", True)):
                 mine = getattr(self, k)
                 if mx and self.state_bits == 8:
@@ -246,8 +252,22 @@ class TensorAdam:
                     B.mx8_encode(arr[k], mine, getattr(self, scale), root=root, rounding="nearest")
                 else:
                     mine.copy_(arr[k])
+            if mx and self.state_bits == 32 and bool(self.exp_avg_sq.isinf().any()):
+                root = torch.empty_like(self.exp_avg_sq)
+                B.mx8_decode(arr["exp_avg_sq"], arr["sq_scale"], root)
+                self._cut_variances(self.exp_avg, self.exp_avg_sq, root)
             self._write_control(B.ctl_from_bytes(raw))
             torch.cuda.synchronize(self.device)
+
+    @staticmethod
+    def _cut_variances(m, v, root=None):
+        """Variances past float32's range (inf) become its largest value, and
+        their momenta shrink in the same proportion to the variance's root
+        2^64; where the root is not known, to no more than that."""
+        import torch
+        past = v.isinf()
+        m.copy_(torch.where(past, m.clamp(-2.0 ** 64, 2.0 ** 64) if root is None else m * (2.0 ** 64 / root), m))
+        v.masked_fill_(past, torch.finfo(torch.float32).max)
 
     def save(self, path: str):
         """Writes state_dict() to a .npz file (plain arrays, no pickles)."""
