@@ -102,3 +102,25 @@ def test_variance_past_the_range_between_widths(src, dst):
     assert bool(b[1].isfinite().all())
     assert 0 < float((one - before)[6000].abs()) < 1e-3 and 0 < float((b[1] - one)[6000].abs()) < 1e-3
     assert float((b[1] - before).abs().max()) < 2e-2
+
+
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_checkpoint_of_shaped_tensors(state_bits):
+    """Masters and 16-bit copies of different shapes (the list counts elements
+    alone): a load restores all of both."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam
+    torch.manual_seed(2)
+    p = [torch.randn(6, 4, device="cuda"), torch.randn((), device="cuda"), torch.randn(3, 1, 70, device="cuda")]
+    g = [torch.randn(x.numel(), device="cuda") for x in p]
+    w = [x.reshape(shape).bfloat16() for x, shape in zip(p, ((-1,), (1, 1), (7, 30)))]
+    a = TensorAdam(p, g, w, state_bits=state_bits, lr=0.1)
+    a.step()
+    sd = a.state_dict()
+    want = [x.clone() for x in p + w]
+    for x in p + w:
+        x.zero_()
+    a.load_state_dict(sd)
+    assert all(torch.equal(x, y) for x, y in zip(p + w, want))
+    a.step()
+    assert not any(torch.equal(x, y) for x, y in zip(p + w, want))

@@ -237,7 +237,7 @@ class TensorAdam:
             for i, (m, n) in enumerate(zip(self.masters, self.numels)):
                 m.detach().view(-1).copy_(arr["master"][at:at + n])
                 if self.params is not None:
-                    self.params[i].detach().copy_(m.detach())
+                    self.params[i].detach().view(-1).copy_(m.detach().view(-1))
                 at += n
             if not mx and self.state_bits == 8:
                 self._cut_variances(arr["exp_avg"], arr["exp_avg_sq"])
