@@ -124,3 +124,40 @@ def test_checkpoint_of_shaped_tensors(state_bits):
     assert all(torch.equal(x, y) for x, y in zip(p + w, want))
     a.step()
     assert not any(torch.equal(x, y) for x, y in zip(p + w, want))
+
+
+# --------------------------------------------------------------- other streams
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_reads_wait_for_steps_on_other_streams(state_bits):
+    """Steps given to a side stream, and at once, from the current stream,
+    what they left: the control block, the whole state, another step count
+    and a load (which no step under way may overwrite)."""
+    torch = torch_mod()
+    a, b = _adam_pair(state_bits, n=20000001, seed=6)
+    x = (torch.randn(a[2].shape, device="cuda") * 1e-3).bfloat16()
+    for o in (a, b):
+        o[2].copy_(x)
+    for _ in range(12):
+        b[0].step()
+    torch.cuda.synchronize()
+    first = a[0].state_dict()
+    side = torch.cuda.Stream()
+
+    def steps():
+        for _ in range(12):
+            a[0].step(stream=side)
+
+    steps()
+    got = a[0].state_dict()
+    torch.cuda.synchronize()
+    want = b[0].state_dict()
+    assert set(got) == set(want) and all(np.array_equal(got[k], want[k]) for k in want)
+    steps()
+    a[0].load_state_dict(first)
+    again = a[0].state_dict()
+    assert all(np.array_equal(again[k], first[k]) for k in first)
+    steps()
+    assert a[0].control() == b[0].control()
+    steps()
+    a[0].set_step(3)
+    assert a[0].control()["t"] == 3

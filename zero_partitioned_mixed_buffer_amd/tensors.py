@@ -167,13 +167,19 @@ class TensorAdam:
                                                 B.ROUNDING[self.rounding], self.seed, self._ws, B._stream(stream)),
                  "zero_tensors_adam_step")
 
+    def _wait(self):
+        """Every stream of the device: a step may run on any of them."""
+        import torch
+        torch.cuda.synchronize(self.device)
+
     def control(self) -> dict:
         """Reads the device control block (synchronises with the device)."""
+        self._wait()
         return B.ctl_from_bytes(bytes(self.ctl.cpu().numpy().tobytes()))
 
     def set_step(self, t: int):
         """Makes ``t`` the number of steps taken so far (beta powers as t
-        successive products)."""
+        successive products).  Synchronises with the device."""
         if t < 0:
             raise ValueError("a negative step count")
         c = self.control()
@@ -193,6 +199,7 @@ class TensorAdam:
         for 8 bits) and the control block.  Synchronises with the device."""
         import numpy as np
         import torch
+        self._wait()
 
         def host(x):
             return (x if x.dtype == torch.float32 else x.view(torch.uint8)).cpu().numpy()
@@ -212,7 +219,8 @@ class TensorAdam:
         gradient above 1e19 was met) is then taken as its largest value and
         its momentum cut with it, so that the weight's next updates keep
         their size, or stay below lr where that size is lost too (an infinite
-        32-bit variance).  The 16-bit copies are written anew."""
+        32-bit variance).  The 16-bit copies are written anew.  Synchronises
+        with the device."""
         import numpy as np
         import torch
         if [int(x) for x in np.asarray(sd["numels"])] != self.numels:
@@ -231,6 +239,7 @@ class TensorAdam:
             a = np.asarray(sd[k])
             if a.dtype != kind or a.shape != (n,):
                 raise ValueError(f"{k}: expected {np.dtype(kind).name}[{n}], got {a.dtype}{list(a.shape)}")
+        self._wait()
         with torch.cuda.device(self.device):
             arr = {k: torch.from_numpy(np.ascontiguousarray(sd[k])).to(self.device) for k in want}
             at = 0
@@ -257,7 +266,7 @@ class TensorAdam:
                 B.mx8_decode(arr["exp_avg_sq"], arr["sq_scale"], root)
                 self._cut_variances(self.exp_avg, self.exp_avg_sq, root)
             self._write_control(B.ctl_from_bytes(raw))
-            torch.cuda.synchronize(self.device)
+            self._wait()
 
     @staticmethod
     def _cut_variances(m, v, root=None):
