@@ -161,3 +161,35 @@ def test_reads_wait_for_steps_on_other_streams(state_bits):
     steps()
     a[0].set_step(3)
     assert a[0].control()["t"] == 3
+
+
+def test_shard_reads_wait_for_steps_on_other_streams():
+    """The same of the flat window's shard."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import OwnedShard
+    n, nd = 8000000, 4
+    p0 = torch.randn(n, device="cuda") * 0.02
+    a, b = (OwnedShard(p0, loss_scale=1.0) for _ in range(2))
+    slices = (torch.randn(nd, n, device="cuda") * 1e-3).half()
+    ag = torch.zeros(n, dtype=torch.float16, device="cuda")
+    for _ in range(12):
+        b.step(slices, allgather=ag)
+    torch.cuda.synchronize()
+    first = a.state_dict()
+    side = torch.cuda.Stream()
+
+    def steps():
+        for _ in range(12):
+            a.step(slices, allgather=ag, stream=side)
+
+    steps()
+    got = a.state_dict()
+    torch.cuda.synchronize()
+    want = b.state_dict()
+    assert all(np.array_equal(got[k], want[k]) for k in want)
+    steps()
+    a.load_state_dict(first)
+    again = a.state_dict()
+    assert all(np.array_equal(again[k], first[k]) for k in ("master", "exp_avg", "exp_avg_sq"))
+    steps()
+    assert a.control()["t"] == 12

@@ -71,8 +71,14 @@ class OwnedShard:
         """fp16 copy of the committed master into the all-gather buffer."""
         B.emit_fp16(self.committed()[0], self.n, allgather, allgather_off, stream)
 
+    def _wait(self):
+        """Every stream of the device: a step may run on any of them."""
+        import torch
+        torch.cuda.synchronize(self.ctl.device)
+
     def control(self) -> dict:
         """Reads the device control block (synchronises with the device)."""
+        self._wait()
         return B.ctl_from_bytes(bytes(self.ctl.cpu().numpy().tobytes()))
 
     def committed(self, ctl: Optional[dict] = None):
@@ -95,7 +101,8 @@ class OwnedShard:
     def load_state_dict(self, sd: dict):
         """Restores a state_dict of a window of the same size: the state goes
         to buffer set 0 and the control block is restored with cur = 0, so
-        the next step continues exactly where the saved shard left off."""
+        the next step continues exactly where the saved shard left off.
+        Synchronises with the device."""
         import numpy as np
         import torch
         for k in ("master", "exp_avg", "exp_avg_sq"):
@@ -108,10 +115,11 @@ class OwnedShard:
         fields = B.ctl_from_bytes(raw)
         fields["cur"] = 0
         dev = self.master[0].device
+        self._wait()
         for dst, k in ((self.master[0], "master"), (self.exp_avg[0], "exp_avg"), (self.exp_avg_sq[0], "exp_avg_sq")):
             dst.copy_(torch.from_numpy(np.ascontiguousarray(sd[k])).to(dev))
         self.ctl.copy_(torch.frombuffer(bytearray(B.ctl_to_bytes(fields)), dtype=torch.uint8).to(dev))
-        torch.cuda.synchronize(dev)
+        self._wait()
 
     def save(self, path: str):
         """Writes state_dict() to a .npz file (plain arrays, no pickles)."""
