@@ -193,3 +193,33 @@ def test_shard_reads_wait_for_steps_on_other_streams():
     assert all(np.array_equal(again[k], first[k]) for k in ("master", "exp_avg", "exp_avg_sq"))
     steps()
     assert a.control()["t"] == 12
+
+
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_first_step_on_another_stream(state_bits):
+    """Made while its stream still has work to do, and stepped at once on
+    another one: the states and tables are there."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import OwnedShard, TensorAdam
+    n = 3000001
+    p0 = torch.randn(n, device="cuda") * 0.02
+    g = (torch.randn(n, device="cuda") * 1e-3).half()
+    slices = g.view(1, n)
+    busy = torch.zeros(1 << 30, device="cuda")
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (None, side):
+        p, ag = p0.clone(), torch.zeros(n, dtype=torch.float16, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(20):  # about 30 ms
+            busy.add_(1.0)
+        opt = TensorAdam([p], [g], state_bits=state_bits, seed=8)
+        opt.step(stream=stream)
+        for _ in range(20):
+            busy.add_(1.0)
+        shard = OwnedShard(p0, loss_scale=1.0)
+        shard.step(slices, allgather=ag, stream=stream)
+        torch.cuda.synchronize()
+        assert opt.control()["t"] == shard.control()["t"] == 1
+        got.append([p, ag, opt.exp_avg.view(torch.uint8), opt.exp_avg_sq.view(torch.uint8), *shard.committed()])
+    assert all(torch.equal(x, y) for x, y in zip(*got))

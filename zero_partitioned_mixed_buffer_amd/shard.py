@@ -37,6 +37,8 @@ class OwnedShard:
                             scale_growth, scale_backoff)
         self.clipped = max_grad_norm > 0
         self.grad_buf = torch.empty(n, dtype=torch.float32, device=dev) if self.clipped else None
+        # the buffers are filled before a step on any stream
+        torch.cuda.current_stream(dev).synchronize()
 
     def step(self, slices, loss_scale: float = 1.0, elem_off: int = 0, allgather=None, allgather_off: int = 0,
              stream=None):

@@ -84,6 +84,8 @@ class TensorAdam:
         self.rounding = rounding if state_bits == 8 else "nearest"
         self.seed = int(seed) & (2**64 - 1)
         self._plan()
+        # the buffers are filled before a step on any stream
+        torch.cuda.current_stream(dev).synchronize()
 
     def _tensor_list(self, grads):
         import torch
