@@ -8,7 +8,7 @@ import pytest
 from oracle import tensor_oracle as to
 
 from gpu_util import torch_mod
-from test_gpu_tensors import Lists, _adam_pair, bits
+from test_gpu_tensors import Lists, _adam_pair, _same, bits
 
 pytestmark = pytest.mark.gpu
 
@@ -223,3 +223,55 @@ def test_first_step_on_another_stream(state_bits):
         assert opt.control()["t"] == shard.control()["t"] == 1
         got.append([p, ag, opt.exp_avg.view(torch.uint8), opt.exp_avg_sq.view(torch.uint8), *shard.committed()])
     assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+def test_checkpoint_brings_the_random_words(rounding, tmp_path):
+    """A list of another seed, rounding and offsets goes on exactly as the one
+    that was saved."""
+    torch = torch_mod()
+    other = "stochastic" if rounding == "nearest" else "nearest"
+    a = _adam_pair(8, seed=2 ** 64 - 3, rounding=rounding, flat_offs=[5, 2 ** 40, 7])[0]
+    b = _adam_pair(8, seed=78, rounding=other)[0]
+    c = _adam_pair(8, seed=79, rounding=rounding, flat_offs=[0, 33, 5000])[0]
+    x = (torch.randn(a[2].shape, device="cuda") * 1e-3).bfloat16()
+    for o in (a, b, c):
+        o[2].copy_(x)
+    a[0].step()
+    a[0].save(str(tmp_path / "s.npz"))
+    b[0].load(str(tmp_path / "s.npz"))
+    c[0].load_state_dict(a[0].state_dict())
+    assert b[0].rounding == rounding and b[0].seed == 2 ** 64 - 3 and b[0].flat_offs == [5, 2 ** 40, 7]
+    for t in range(2):
+        for o in (a, b, c):
+            o[0].step()
+        torch.cuda.synchronize()
+        _same(a, b)
+        _same(a, c)
+    b[0].set_grads([g.clone() for g in b[0].grads])  # the offsets stay
+    for o in (a, b):
+        o[0].step()
+    torch.cuda.synchronize()
+    _same(a, b)
+
+
+def test_checkpoint_refusals_leave_the_list_as_it_was():
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import binding as B
+    a, b = _adam_pair(8, seed=3), _adam_pair(8, seed=4)
+    a, b, c = a[0], b[0], b[1]
+    a[2].normal_(0, 1e-3)
+    a[0].step()
+    sd = a[0].state_dict()
+    for bad, kind in ((dict(rounding=np.asarray("up")), ValueError), (dict(flat_offs=np.array([0, 1])), ValueError),
+                      (dict(flat_offs=np.array([0, 33, -1])), B.ZeroError), (dict(exp_avg=sd["exp_avg"][1:]), ValueError),
+                      (dict(ctl=sd["ctl"][1:]), ValueError)):
+        with pytest.raises(kind):
+            b[0].load_state_dict({**sd, **bad})
+        torch.cuda.synchronize()
+        _same(b, c)
+        assert b[0].seed == 4 and b[0].rounding == "stochastic"
+    # a state_dict without the words' parameters: the list keeps its own
+    b[0].load_state_dict({k: v for k, v in sd.items() if k not in ("seed", "rounding", "flat_offs")})
+    _same(a, b)
+    assert b[0].seed == 4

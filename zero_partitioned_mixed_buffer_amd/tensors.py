@@ -87,7 +87,7 @@ class TensorAdam:
         # the buffers are filled before a step on any stream
         torch.cuda.current_stream(dev).synchronize()
 
-    def _tensor_list(self, grads):
+    def _tensor_list(self, grads, flat_offs=None):
         import torch
         mx = self.state_bits == 8
         with torch.cuda.device(self.device):
@@ -108,7 +108,8 @@ class TensorAdam:
                     base, size = flat.data_ptr(), flat.element_size()
                     columns[name] = [base + o // per * size for o in self.state_offs]
                     keep.append(flat)
-            return B._plan_list(numels, columns, gtype, ptype, B.TYPE_MX8 if mx else B.TYPE_F32, self.flat_offs, keep)
+            return B._plan_list(numels, columns, gtype, ptype, B.TYPE_MX8 if mx else B.TYPE_F32,
+                                self.flat_offs if flat_offs is None else flat_offs, keep)
 
     def _plan(self):
         self.list = self._tensor_list(self.grads)
@@ -117,6 +118,16 @@ class TensorAdam:
         self._head = (self.list.ref, table)
         self._checks = (self.overflow.data_ptr(), self.sumsq.data_ptr())
         self._ctl, self._ws = self.ctl.data_ptr(), self.workspace.data_ptr()
+
+    def _offs(self):
+        """The tensors' first random counters (by default packed in list order)."""
+        if self.flat_offs is not None:
+            return self.flat_offs
+        at, offs = 0, []
+        for n in self.numels:
+            offs.append(at)
+            at += n
+        return offs
 
     def set_grads(self, grads: Sequence):
         """Other gradient tensors of the same sizes and dtype, from the next
@@ -198,7 +209,9 @@ class TensorAdam:
     # ------------------------------------------------------------ checkpoint
     def state_dict(self) -> dict:
         """Host copies of the weights, states (codes and scale bytes as uint8
-        for 8 bits) and the control block.  Synchronises with the device."""
+        for 8 bits) and the control block; for 8 bits also what the random
+        words depend on (seed, rounding and flat_offs).  Synchronises with
+        the device."""
         import numpy as np
         import torch
         self._wait()
@@ -212,16 +225,21 @@ class TensorAdam:
                "ctl": np.frombuffer(self.ctl.cpu().numpy().tobytes(), dtype=np.uint8).copy()}
         if self.state_bits == 8:
             out["avg_scale"], out["sq_scale"] = host(self.avg_scale), host(self.sq_scale)
+            out["seed"], out["rounding"] = np.uint64(self.seed), np.asarray(self.rounding)
+            out["flat_offs"] = np.asarray(self._offs(), dtype=np.int64)
         return out
 
     def load_state_dict(self, sd: dict):
         """Restores a state_dict of a list of the same sizes.  Of the same
-        state_bits it resumes exactly; states of the other width are encoded
-        (to nearest) or decoded.  A variance that float32 does not hold (a
-        gradient above 1e19 was met) is then taken as its largest value and
-        its momentum cut with it, so that the weight's next updates keep
-        their size, or stay below lr where that size is lost too (an infinite
-        32-bit variance).  The 16-bit copies are written anew.  Synchronises
+        state_bits, under the same hyperparameters, it resumes exactly: 8-bit
+        states bring their seed, rounding and flat_offs along (a step captured
+        in a graph keeps the seed and rounding it was captured with).  States
+        of the other width are encoded (to nearest) or decoded; a variance
+        that float32 does not hold (a gradient above 1e19 was met) is then
+        taken as its largest value and its momentum cut with it, so that the
+        weight's next updates keep their size, or stay below lr where that
+        size is lost too (an infinite 32-bit variance).  The 16-bit copies
+        are written anew.  Synchronises
         with the device."""
         import numpy as np
         import torch
@@ -241,6 +259,13 @@ class TensorAdam:
             a = np.asarray(sd[k])
             if a.dtype != kind or a.shape != (n,):
                 raise ValueError(f"{k}: expected {np.dtype(kind).name}[{n}], got {a.dtype}{list(a.shape)}")
+        words = None
+        if mx and self.state_bits == 8 and "seed" in sd:
+            words = (int(np.asarray(sd["seed"])), str(np.asarray(sd["rounding"])),
+                     [int(x) for x in np.asarray(sd["flat_offs"])])
+            B._rounding(words[1])
+            # planned before anything is written: wrong offsets are refused
+            new = self._tensor_list(self.grads, words[2]) if words[2] != self._offs() else None
         self._wait()
         with torch.cuda.device(self.device):
             arr = {k: torch.from_numpy(np.ascontiguousarray(sd[k])).to(self.device) for k in want}
@@ -267,6 +292,12 @@ class TensorAdam:
                 root = torch.empty_like(self.exp_avg_sq)
                 B.mx8_decode(arr["exp_avg_sq"], arr["sq_scale"], root)
                 self._cut_variances(self.exp_avg, self.exp_avg_sq, root)
+            if words is not None:
+                self.seed, self.rounding = words[0] & (2**64 - 1), words[1]
+                if new is not None:
+                    self.flat_offs, self.list.tensors = words[2], new.tensors
+                    if new.table is not None:
+                        self.list.table.copy_(new.table)
             self._write_control(B.ctl_from_bytes(raw))
             self._wait()
 
