@@ -275,3 +275,37 @@ def test_checkpoint_refusals_leave_the_list_as_it_was():
     b[0].load_state_dict({k: v for k, v in sd.items() if k not in ("seed", "rounding", "flat_offs")})
     _same(a, b)
     assert b[0].seed == 4
+
+
+# -------------------------------------------------------------------- autograd
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_backward_through_a_step_raises(state_bits):
+    """A graph that saved a weight or its 16-bit copy before a step refuses
+    its backward pass, as after torch's own in-place operations; one made
+    after it runs."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam, binding as B
+    torch.manual_seed(4)
+    p = torch.nn.Parameter(torch.randn(40, 5, device="cuda"))
+    w = torch.nn.Parameter(p.detach().bfloat16())
+    p.grad = torch.randn_like(p)
+    opt = TensorAdam([p], [p.grad], [w], state_bits=state_bits)
+    for x in (p, w):
+        y = (x * x).sum()
+        opt.step()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    lst = opt.list
+    y = (p * p).sum()
+    B.tensors_adam_step(lst, opt.hp, opt.ctl, opt.workspace)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    w.grad = None
+    (w * w).sum().backward()
+    assert torch.equal(w.grad, 2 * w.detach())
+    # tensors that no graph knows are not counted
+    q = torch.randn(100, device="cuda")
+    plain = TensorAdam([q], [torch.randn(100, device="cuda")], state_bits=state_bits)
+    at = q._version
+    plain.step()
+    assert q._version == at and not plain.list.written

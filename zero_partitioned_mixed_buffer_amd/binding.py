@@ -534,14 +534,23 @@ def _grad_column(grads: Sequence) -> Tuple[int, List[int], List[int]]:
 
 class TensorList:
     """A planned list of tensors: its table in device memory, and the tensors
-    it points to (kept alive here).  Made by tensor_list()."""
+    it points to (kept alive here).  Made by tensor_list().  ``written``:
+    those of the tensors that a step writes and that require gradients."""
 
-    def __init__(self, info: TensorListInfo, table, tensors):
+    def __init__(self, info: TensorListInfo, table, tensors, written=()):
         self.info = info
         self.ref = C.byref(info)
         self.table = table
         self.tensors = tensors
+        self.written = [t for t in written if t.requires_grad]
         self.numel = int(info.n_elems)
+
+    def count_write(self):
+        """Tells autograd of a step: a backward pass through a graph that has
+        saved one of the weights before it raises."""
+        if self.written:
+            from torch.autograd.graph import increment_version
+            increment_version(self.written)
 
 
 def tensor_list(grads: Sequence, masters: Optional[Sequence] = None, params: Optional[Sequence] = None,
@@ -581,11 +590,11 @@ def tensor_list(grads: Sequence, masters: Optional[Sequence] = None, params: Opt
             _, columns["sq_scale"] = _column(sq_scale, numels, _SCALES, "sq_scale", MX8_BLOCK)
         keep += [list(c) for c in (masters, params, exp_avg, exp_avg_sq, avg_scale, sq_scale) if c is not None]
     _on_current(keep)
-    return _plan_list(numels, columns, gtype, ptype, stype, flat_offs, keep)
+    return _plan_list(numels, columns, gtype, ptype, stype, flat_offs, keep, (*(masters or ()), *(params or ())))
 
 
 def _plan_list(numels: Sequence[int], columns: dict, gtype: int, ptype: int, stype: int,
-               flat_offs: Optional[Sequence[int]], keep) -> TensorList:
+               flat_offs: Optional[Sequence[int]], keep, written=()) -> TensorList:
     """The list of tensors at the addresses in ``columns`` (zero_tensor's
     fields), its table uploaded to the current device."""
     import numpy as np
@@ -606,12 +615,12 @@ def _plan_list(numels: Sequence[int], columns: dict, gtype: int, ptype: int, sty
     if st not in (ZERO_OK, ZERO_ECAPACITY):
         _check(st, "zero_tensors_plan")
     if info.table_bytes == 0:
-        return TensorList(info, None, keep)
+        return TensorList(info, None, keep, written)
     host = torch.empty(int(info.table_bytes) + 16, dtype=torch.uint8)
     host = host[-host.data_ptr() % 16:][:int(info.table_bytes)]
     _check(lib().zero_tensors_plan(tensors, count, gtype, ptype, stype, C.byref(info), host.data_ptr(), host.numel()),
            "zero_tensors_plan")
-    return TensorList(info, host.to(torch.device("cuda", torch.cuda.current_device())), keep)
+    return TensorList(info, host.to(torch.device("cuda", torch.cuda.current_device())), keep, written)
 
 
 def tensors_grad_norm(lst: TensorList, overflow, sumsq, workspace, loss_scale: float = 1.0, ctl=None, stream=None):
@@ -642,7 +651,9 @@ def _rounding(name: str) -> int:
 
 def tensors_adam_step(lst: TensorList, hp: AdamHp, ctl, workspace, loss_scale: float = 1.0, overflow=None,
                       sumsq=None, rounding: str = "nearest", seed: int = 0, stream=None):
-    """One Adam/AdamW step of every tensor of the list, in place."""
+    """One Adam/AdamW step of every tensor of the list, in place.  Weights and
+    copies that required gradients when the list was made count it as torch's
+    in-place operations do (skipped steps too; a graph's replays do not)."""
     cur = _current_device()
     _check_operand(overflow, 1, ("int32",), "overflow flag", cur)
     _check_operand(sumsq, 1, ("float64",), "sum of squares", cur)
@@ -654,6 +665,7 @@ def tensors_adam_step(lst: TensorList, hp: AdamHp, ctl, workspace, loss_scale: f
                                         _ptr(ctl), _ptr(overflow), _ptr(sumsq), _rounding(rounding),
                                         int(seed) & (2**64 - 1), _ptr(workspace), _stream(stream)),
            "zero_tensors_adam_step")
+    lst.count_write()
 
 
 def _check_mx8(x, codes, scales):

@@ -34,6 +34,11 @@ class TensorAdam:
     with).  Lists that share one norm, or ranks that hold parts of the
     parameters, take it apart from the step: grad_norm() on each, then the
     sums added and the flags OR-ed, then step(norm=...).
+
+    Masters and params that require gradients (when the list is made) count
+    each step as torch's in-place operations do, so that a backward pass
+    through a graph made before it raises; aliases that do not (p.data,
+    p.detach()) and replays of a captured step are not counted.
     """
 
     def __init__(self, masters: Sequence, grads: Sequence, params: Optional[Sequence] = None,
@@ -109,7 +114,8 @@ class TensorAdam:
                     columns[name] = [base + o // per * size for o in self.state_offs]
                     keep.append(flat)
             return B._plan_list(numels, columns, gtype, ptype, B.TYPE_MX8 if mx else B.TYPE_F32,
-                                self.flat_offs if flat_offs is None else flat_offs, keep)
+                                self.flat_offs if flat_offs is None else flat_offs, keep,
+                                (*self.masters, *(self.params or ())))
 
     def _plan(self):
         self.list = self._tensor_list(self.grads)
@@ -179,6 +185,7 @@ class TensorAdam:
         B._check(B.lib().zero_tensors_adam_step(*self._head, C.byref(self.hp), self.loss_scale, self._ctl, *checks,
                                                 B.ROUNDING[self.rounding], self.seed, self._ws, B._stream(stream)),
                  "zero_tensors_adam_step")
+        self.list.count_write()
 
     def _wait(self):
         """Every stream of the device: a step may run on any of them."""
