@@ -471,17 +471,23 @@ int zero_gather_layers(const uint16_t* const* windows, int32_t nd, int64_t part,
  * bits, 3 mantissa bits, largest finite value 448).  An encoded block has
  * the smallest e >= 1 that keeps its largest magnitude within 448 scales;
  * at the largest such scale, 2^120, a magnitude past 240 scales keeps 240
- * (the next code, 256, would read as inf);
- * a block that holds an inf or a NaN has e = 255 and every code NaN.  A
- * positive root keeps at least the smallest positive code, since a root of
- * 0 would turn the next update into m / eps.
+ * (the next code, 256, would read as inf); a block that holds an inf or a
+ * NaN has e = 255 and every code NaN.  A positive root keeps at least the
+ * smallest positive code, since a root of 0 would turn the next update into
+ * m / eps.
  *
  * Rounding of 8-bit states: ZERO_ROUND_NEAREST (ties to even), or
  * ZERO_ROUND_STOCHASTIC, which rounds up with the probability of the part
- * that is cut off (in steps of 2^-20).  With beta2 = 0.999 a step changes a
- * variance by about a thousandth, far less than half a step of an e4m3
- * root, so that nearest rounding leaves it where it is; stochastic rounding
- * moves it right on average.  The random word of element i is
+ * that is cut off, counted in steps of 2^-20 for a momentum and of 2^-16 for
+ * a root (what is below such a step is cut off for good).  With beta2 =
+ * 0.999 a step changes a variance by about a thousandth, far less than half
+ * a step of an e4m3 root, so that nearest rounding leaves it where it is;
+ * stochastic rounding moves it right on average, short by less than 2^-16 of
+ * a code's step each time.  A root of 8 to 16 such steps (2^-6 scales or more)
+ * that decays by (1 - beta2) / 2 thus decays too fast by less than
+ * 2^-18 / (1 - beta2) of that: 0.4% at beta2 = 0.999, 4% at 0.9999.  Above
+ * 0.9999 variances drift low; fp32 states hold them.  The random word of
+ * element i is
  *   mix(c ^ k1, k2),  c = (flat_off + i) mod 2^32,
  *   k1 = mix(lo(seed) ^ mix(hi(seed) ^ mix(step, 0), 0), 0),  k2 = mix(~k1, 0),
  *   mix(x, k): x ^= x >> 16; x *= 0xACE5F457; x ^= (x >> 15) ^ k;

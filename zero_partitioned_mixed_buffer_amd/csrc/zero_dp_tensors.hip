@@ -18,8 +18,8 @@
 //   encode   blocks of 32 fp32 values: scale 2^(e-127) with the smallest e >= 1
 //            that keeps the largest magnitude within 448 scales, each value
 //            over the scale in e4m3 (nearest, or stochastic: the random word's
-//            top 20 bits added to the 20 bits that are cut off), at most
-//            240 at scale 2^120
+//            top 20 bits, for a root its low 16 with four zeros behind, added
+//            to the 20 bits that are cut off), at most 240 at scale 2^120
 //   decode   value = code * scale, squared for a root
 //
 // Everything here is a stream over memory.  No two workgroups write the same

@@ -23,7 +23,9 @@ class TensorAdam:
     The states lie in one buffer each (``exp_avg``, ``exp_avg_sq``; with
     state_bits=8 also ``avg_scale`` and ``sq_scale``), tensor i from element
     state_offs[i], a multiple of 64, with zeros in the gaps.  With 8 bits
-    ``exp_avg_sq`` holds the variance's root.  Fill them in place.
+    ``exp_avg_sq`` holds the variance's root, under stochastic rounding for a
+    beta2 of at most 0.9999 (above it variances drift low).  Fill them in
+    place.
 
     check_finite (default) takes a pass over the gradients first and skips
     the step if any is inf or NaN; max_grad_norm > 0 (clipping) and
