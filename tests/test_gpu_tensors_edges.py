@@ -309,3 +309,34 @@ def test_backward_through_a_step_raises(state_bits):
     at = q._version
     plain.step()
     assert q._version == at and not plain.list.written
+
+
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_gradients_made_anew_each_step(state_bits):
+    """A loop with zero_grad()'s default: autograd's new gradients, named by
+    set_grads, step as the same values copied into the first ones do."""
+    torch = torch_mod()
+    from zero_partitioned_mixed_buffer_amd import TensorAdam
+    torch.manual_seed(1)
+    net = torch.nn.Sequential(torch.nn.Linear(33, 70), torch.nn.Tanh(), torch.nn.Linear(70, 5)).cuda()
+    params = list(net.parameters())
+    twins = [p.detach().clone() for p in params]
+    held = [torch.zeros_like(p) for p in twins]
+    for p in params:
+        p.grad = torch.zeros_like(p)
+    a = TensorAdam(params, [p.grad for p in params], state_bits=state_bits, seed=3)
+    b = TensorAdam(twins, held, state_bits=state_bits, seed=3)
+    keep = [p.grad for p in params]  # so that no new gradient can take an old one's place
+    for t in range(4):
+        net.zero_grad()
+        net(torch.randn(64, 33, device="cuda")).square().mean().backward()
+        assert all(p.grad.data_ptr() != g.data_ptr() for p, g in zip(params, keep))
+        a.set_grads([p.grad for p in params])
+        keep = [p.grad for p in params]
+        for h, p in zip(held, params):
+            h.copy_(p.grad)
+        a.step()
+        b.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p.detach(), q) for p, q in zip(params, twins))
+        assert a.control() == b.control() and a.control()["t"] == t + 1

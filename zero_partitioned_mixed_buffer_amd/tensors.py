@@ -3,7 +3,8 @@
 Holds the list's states, control block and workspace (allocated with torch)
 and forwards each step to the library: zero_tensors_grad_norm where the
 gradients are checked or clipped, then zero_tensors_adam_step.  Nothing here
-synchronises with the device but control() and the checkpoint calls.
+synchronises with the device but the constructor, set_grads(), set_step(),
+control() and the checkpoint calls.
 """
 from __future__ import annotations
 
@@ -26,6 +27,12 @@ class TensorAdam:
     ``exp_avg_sq`` holds the variance's root, under stochastic rounding for a
     beta2 of at most 0.9999 (above it variances drift low).  Fill them in
     place.
+
+    The list holds the tensors' addresses.  Gradients that autograd makes anew
+    (after zero_grad() with its default, set_to_none=True) are others than
+    those it was given: either zero_grad(set_to_none=False) keeps the tensors,
+    or set_grads() names the new ones after each backward pass.  Without
+    either, steps go on with the old gradients.
 
     check_finite (default) takes a pass over the gradients first and skips
     the step if any is inf or NaN; max_grad_norm > 0 (clipping) and
