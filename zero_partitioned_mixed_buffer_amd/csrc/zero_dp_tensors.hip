@@ -114,7 +114,7 @@ __device__ __forceinline__ uint32_t max8(uint32_t x) {
 // Draws a ticket for the workgroup (one thread of it): true for the last of
 // the grid, which leaves the counters at zero.  Draws on one address follow
 // each other at about 10 ns, so the workgroups draw from 32 counters, and
-// the last of each draws from the one behind them (600 workgroups: 15.9 us
+// the last of each draws from the one behind them (755 workgroups: 15.9 us
 // of kernel on one counter, 12.5 on 33).  The order is relaxed: what has
 // to be seen by the last workgroup has to be performed before the draw.
 __device__ __forceinline__ bool last_to_draw(uint32_t* ticket) {
@@ -187,7 +187,8 @@ __device__ __forceinline__ float float_of(uint32_t x) { return __builtin_bit_cas
 // multiples of a unit larger than u^2/4, and likewise at s + u/2; one fused
 // multiply-add gives the sign.  Nothing underflows in it from 2^-96 up (and
 // at 0); a wave that holds a smaller value takes the library's root, which
-// scales first.
+// scales first.  (The compiler's own expansion of a correctly rounded root
+// takes the same correction, after a scaling that few values here need.)
 __device__ __forceinline__ void roots4(fvec& x) {
     uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
@@ -431,9 +432,9 @@ __device__ __forceinline__ void load_grads(GradVec<kGrad> (&v)[kRows], gcu8 g, i
 
 // The list is walked from its end, and its first kKeep bytes of gradients
 // are read with ordinary loads, so that the step that follows finds them in
-// the 256 MB Infinity Cache: for GPT-2 small the norm takes 51 us instead of
-// 45, and norm and step together 620 instead of 650 (32-bit states) and 410
-// instead of 430 (8-bit).  Kept throughout, the GPT-2 XL norm loses 4%.
+// the 256 MB Infinity Cache: for GPT-2 small the norm takes 50 us instead of
+// 44, and norm and step together 624 instead of 650 (32-bit states) and 400
+// instead of 424 (8-bit); the GPT-2 XL norm 453 instead of 448.
 constexpr int64_t kKeep = 192ll << 20;
 
 // Sum of squares of a list.  Bound by HBM reads: one load, two conversions and
@@ -744,11 +745,12 @@ __device__ __forceinline__ void finish_chunk(Row<kGrad, kMx> (&r)[kRows], const 
 // chunk's are on their way (kPipe).  4096 elements a chunk: 2048 measured 6%
 // (fp32 states) and 2% (8-bit) slower, 8192 4% and 12%.
 //   fp32 states, f16 gradients and copy: 28 bytes an element, GPT-2 small
-//     582 us, 6.0 TB/s, VALU 37% busy
-//   8-bit states, bf16 gradients and copy: 16.1 bytes, GPT-2 small 370 us, 5.4
-//     TB/s, VALU 68% busy; a quarter of GPT-2 XL 1206 us, 5.2 TB/s
+//     575 us, 6.1 TB/s, VALU 37% busy
+//   8-bit states, bf16 gradients and copy: 16.1 bytes, GPT-2 small 372 us, 5.4
+//     TB/s, VALU 69% busy; a quarter of GPT-2 XL 1216 us, 5.2 TB/s
 // Short lists are bound by latency: table, descriptor and data in turn, then
-// the stores (400 tensors, 1.4e6 elements: 14.4 and 11.9 us of kernel).
+// the stores (400 tensors: 14.3 us of kernel for 1.4e6 elements with fp32
+// states, 12.1 for 1.8e6 with 8-bit ones).
 template <int kGrad, int kParam, bool kMx, bool kStoch, bool kPipe>
 __global__ void __launch_bounds__(kBlock) tensors_adam_kernel(ListArgs list, TensorStepArgs a, int64_t from, int64_t to) {
     const bool skip = a.overflow != nullptr && *a.overflow != 0;
@@ -796,10 +798,10 @@ __global__ void __launch_bounds__(kBlock) tensors_adam_kernel(ListArgs list, Ten
 
 // ------------------------------------------------------- encode and decode
 // Both bound by HBM: 5.03 bytes an element (1.2e8 values: encode 110 us, 5.7
-// TB/s; decode 114 us, 5.5 TB/s, four fifths of it writes).
+// TB/s; decode 115 us, 5.4 TB/s, four fifths of it writes).
 // Rows whose loads are under way together; GPT-2-small-sized arrays, eight
-// workgroups per CU: one row 117 us to encode and 115 to decode, four 110
-// and 113.
+// workgroups per CU: one row 116 us to encode and 113 to decode, four 110
+// and 115.
 constexpr int kMxRows = 4;
 
 template <bool kRoot, bool kStoch>
@@ -919,18 +921,21 @@ int finish_launch() {
 //   norm: 5 (1.56e9 bf16 gradients, all streaming: 443 us; 4: 486, 6: 443, 8: 505)
 //   adam, fp32 states: 1 with the next chunk's loads under way (GPT-2 small:
 //     609 us; 2 such: 656, 4 without the loads ahead: 672)
-//   adam, 8-bit states: 3 (a quarter of GPT-2 XL: 1237 us; 2: 1240, 1: 1454)
+//   adam, 8-bit states: 3 (a quarter of GPT-2 XL: 1237 us; 2: 1240, 1: 1454).
+//     With 16-bit gradients the kernels take up to 168 VGPRs, the most of
+//     which three workgroups fit (174: two, and GPT-2 small 449 us for 397);
+//     with f32 gradients 182, and two fit (GPT-2 small: 411 us).
 constexpr int kNormPerCu = 5;
 constexpr int kAdamPerCu = 1;
 constexpr int kAdamMxPerCu = 3;
 // fp32 states: a list of at most kAdamShortChunks chunks per CU takes more
-// workgroups without loads ahead (400 tensors, 600 chunks: 14.3 us; 17.1 on
-// kAdamPerCu; 2048 chunks: 44.0 and 46.0; 4096: 85.0 and 83.1).
+// workgroups without loads ahead (400 tensors, 673 chunks: 13.9 us; 16.7 on
+// kAdamPerCu; 2048 chunks: 44.8 and 47.1; 4096: 85.1 and 85.4).
 constexpr int kAdamShortChunks = 8;
 constexpr int kAdamShortPerCu = 4;
 // A list of more than twice this many chunks is stepped in launches of
-// about 2^26 elements (a quarter of GPT-2 XL, one launch against six: 1951
-// and 1884 us with fp32 states, 1245 and 1217 with 8-bit ones; GPT-2 small
+// about 2^26 elements (a quarter of GPT-2 XL, one launch against six: 1946
+// and 1875 us with fp32 states, 1231 and 1213 with 8-bit ones; GPT-2 small
 // in two: within 1%; launches of 2^24: 3% to 8% slower).
 constexpr int64_t kPieceChunks = 1 << 14;
 constexpr int kMx8PerCu = 8;
