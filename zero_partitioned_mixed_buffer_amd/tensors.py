@@ -255,8 +255,7 @@ class TensorAdam:
         taken as its largest value and its momentum cut with it, so that the
         weight's next updates keep their size, or stay below lr where that
         size is lost too (an infinite 32-bit variance).  The 16-bit copies
-        are written anew.  Synchronises
-        with the device."""
+        are written anew.  Synchronises with the device."""
         import numpy as np
         import torch
         if [int(x) for x in np.asarray(sd["numels"])] != self.numels:
