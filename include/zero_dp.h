@@ -606,6 +606,126 @@ int zero_mx8_encode(const float* x, int64_t n, int32_t root, uint8_t* codes, uin
                     uint64_t seed, int64_t step, int64_t flat_off, void* stream);
 int zero_mx8_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, int32_t root, float* x, void* stream);
 
+/* ---- 8-bit layer operators --------------------------------------------
+ * A layer's forward and backward products in 8 bits, between the gathered
+ * 16-bit weights (zero_gather_params) and the gradients that a step takes:
+ * the encode of a matrix, the norm whose output is encoded, and the product
+ * of two encoded matrices.  The form is this library's own; the pages hold
+ * 16-bit weights and gradients only.
+ *
+ * A matrix in the 8-bit form (zero_block8) has e4m3 codes (OCP FP8) and one
+ * scale byte e, 2^(e - 127), for each block of 128:
+ *   ZERO_BLOCK8_ROWS   128 consecutive values of a row (activations, gradients);
+ *                      scales[r * scales_stride + c / 128]
+ *   ZERO_BLOCK8_TILES  128 x 128 values (weights; the transposed matrix has the
+ *                      same blocks); scales[(r / 128) * scales_stride + c / 128]
+ * counted from the matrix' first row and column; the last blocks may be
+ * short.  Scales and codes follow ZERO_TYPE_MX8's rule: the smallest e >= 1
+ * that keeps the block's largest magnitude within 448 scales, codes rounded
+ * to nearest even, at most 240 at the scale 2^120; a block that holds an inf
+ * or a NaN has e = 255 and every code NaN.
+ *
+ * Bytes between a row's end and the next row's start are not looked at (they
+ * are read, in whole pieces of 16 bytes of codes and 4 of scales that hold a
+ * byte of the row, but have no effect) and never written.
+ *
+ * Overlap: an output may be the very memory of an input where the call's text
+ * says so (same address, type and stride); any other overlap of an output
+ * with anything else is ZERO_EALIAS.  Two matrices with the same stride in
+ * disjoint columns of one buffer do not overlap.
+ */
+#define ZERO_BLOCK8_ROWS  0
+#define ZERO_BLOCK8_TILES 1
+
+/* rows x cols numbers of `type` (ZERO_TYPE_F32, F16 or BF16), device memory:
+ * element (r, c) at index r * stride + c, aligned to the element.  stride >=
+ * cols; cols <= 2^23, rows < 2^31.  rows or cols may be 0 (data ignored). */
+typedef struct zero_matrix {
+    void* data;
+    int64_t rows, cols, stride;
+    int32_t type, reserved;  /* reserved must be 0 */
+} zero_matrix;
+
+/* rows x cols codes and their scales, device memory.  codes: 16-byte aligned,
+ * codes_stride (bytes) >= cols, a multiple of 16 and at most 2^23.  scales:
+ * 4-byte aligned, scales_stride (bytes) >= ceil(cols / 128), a multiple of 4.
+ * cols <= 2^23, rows < 2^31. */
+typedef struct zero_block8 {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows, cols, codes_stride, scales_stride;
+    int32_t blocks, reserved;  /* reserved must be 0 */
+} zero_block8;
+
+/* x, or x * row_mul[r] * col_mul[c] (fp32, in that order), into the 8-bit form:
+ * `out` as it is, `out_t` transposed (cols x rows); either may be NULL, not
+ * both, and both have the same `blocks`.  x is read once.
+ *   row_mul, col_mul: device, either may be NULL; col_mul of col_type.  With
+ *     zero_rms_norm8's rstd and weight, and x its h, this makes the norm's
+ *     output again, transposed for the weight gradient.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW, ZERO_EALIAS, ZERO_EHIP.
+ */
+int zero_block8_encode(const zero_matrix* x, const float* row_mul, const void* col_mul, int32_t col_type,
+                       const zero_block8* out, const zero_block8* out_t, void* stream);
+
+/* h = x + residual, rounded to their type; rstd[r] = 1 / sqrt(mean over c of
+ * h^2 + eps) (the sum in float64); y = (h * rstd[r]) * weight[c] in fp32, in the
+ * 8-bit form by rows.  Source: the root-mean-square layer norm's definition.
+ *   residual: NULL (then h is x, and `h` must be NULL) or of x's type and size.
+ *   h: of x's type and size; may be x's or residual's memory.
+ *   weight: device, x->cols values of weight_type.  rstd: device float[rows].
+ *   eps: > 0, finite.
+ * A row with an inf or NaN has NaN where its formula does (every block that
+ * holds one is all NaN).  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW,
+ * ZERO_EALIAS, ZERO_EHIP.
+ */
+int zero_rms_norm8(const zero_matrix* x, const zero_matrix* residual, const void* weight, int32_t weight_type,
+                   double eps, const zero_matrix* h, const zero_block8* y, float* rstd, void* stream);
+
+/* The norm's gradients for dy, the gradient of y (the rounding to 8 bits is
+ * passed over), in fp32:
+ *   xh = h * rstd[r];  g = dy * weight;  c = mean over the row of g * xh
+ *   dx = (g - xh * c) * rstd[r] + dh   (x's and residual's gradient, rounded to their type)
+ *   dweight[c] = sum over rows of dy * xh
+ *   dh: the gradient that reaches h another way (the residual path); NULL for none.
+ *   dy, h, dh, dx: one type and size; dx may be dy's or dh's memory.
+ *   dweight: device float[cols]; summed in a fixed order (the same call gives
+ *     the same bits on the same GPU).  NULL: not computed, and workspace may be NULL.
+ *   workspace: device, zero_rms_norm8_workspace_bytes(rows, cols), 16-byte
+ *     aligned; its contents before and after do not matter.
+ * No rows: dweight is 0.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW,
+ * ZERO_EALIAS, ZERO_EHIP.
+ */
+int zero_rms_norm8_backward(const zero_matrix* dy, const zero_matrix* h, const void* weight, int32_t weight_type,
+                            const float* rstd, const zero_matrix* dh, const zero_matrix* dx, float* dweight,
+                            void* workspace, void* stream);
+/* Workspace of the call above (0 for sizes it would refuse). */
+int64_t zero_rms_norm8_workspace_bytes(int64_t rows, int64_t cols);
+
+/* out[m][n] = sum over k of a[m][k] * b[n][k] (+ add[m][n]), rounded once to
+ * out's type.  With z = y W^T: the forward product is a = y, b = W; the input
+ * gradient a = dz, b = W transposed; the weight gradient a = dz transposed, b =
+ * y transposed (zero_block8_encode's out_t).
+ *   a: M x K, b: N x K, either kind of blocks; K = 0 gives add, or 0.
+ *     ceil(M / 256) * ceil(N / 256) <= 2^22.
+ *   add: NULL, or M x N of out's type; may be out's memory.
+ *   out: F16 or BF16: the sum goes over the scaled 8-bit matrix instructions,
+ *     which add the products of neighbouring k to fewer bits than fp32 holds:
+ *     off by less than 2^-10 of the sum of their magnitudes (measured on normal
+ *     data: 2^-16 of the result's size).  F32: codes are widened to bf16, which
+ *     is exact, and summed in fp32, at half that rate; values below 2^-126 may
+ *     read as 0 there.
+ *   workspace: device, zero_block8_workspace_bytes(M, N, K), 16-byte aligned
+ *     (NULL if that is 0); its contents before and after do not matter.
+ * A NaN code or scale reaches its row, or its column, of out.  The same call
+ * gives the same bits.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW,
+ * ZERO_EALIAS, ZERO_EHIP.
+ */
+int zero_block8_product(const zero_block8* a, const zero_block8* b, const zero_matrix* add, const zero_matrix* out,
+                        void* workspace, void* stream);
+/* Workspace of the call above, for any types (0 for sizes it would refuse). */
+int64_t zero_block8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
 /* ---- emit (all-gather half) ------------------------------------------
  * allgather[allgather_off + j] = fp16_RNE(master[j]) for j < n (IEEE
  * round-to-nearest-even, overflow to inf).  Initial fill of the all-gather

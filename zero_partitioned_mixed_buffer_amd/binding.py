@@ -32,6 +32,8 @@ EXPORTED = (
     "zero_emit_fp16", "zero_gather_params", "zero_adam_step_noalloc", "zero_calib_triad",
     "zero_calib_stream_mix", "zero_adam_step_buckets", "zero_gather_layers", "zero_calib_slice_read",
     "zero_tensors_plan", "zero_tensors_grad_norm", "zero_tensors_adam_step", "zero_mx8_encode", "zero_mx8_decode",
+    "zero_block8_encode", "zero_rms_norm8", "zero_rms_norm8_backward", "zero_rms_norm8_workspace_bytes",
+    "zero_block8_product", "zero_block8_workspace_bytes",
 )
 ABI_VERSION = 7
 BUCKET_FIRST = 1
@@ -79,6 +81,8 @@ class Bucket(C.Structure):
 
 MAX_BUCKETS_PER_CALL = 1024
 MX8_BLOCK = 32
+BLOCK8 = 128
+BLOCKS = {"rows": 0, "tiles": 1}
 TYPE_NONE, TYPE_F32, TYPE_F16, TYPE_BF16, TYPE_MX8 = range(5)
 ROUNDING = {"nearest": 0, "stochastic": 1}
 
@@ -92,6 +96,17 @@ class Tensor(C.Structure):
 class TensorListInfo(C.Structure):
     _fields_ = [(k, C.c_int32) for k in ("n_tensors", "grad_type", "param_type", "state_type")] + \
                [(k, C.c_int64) for k in ("n_elems", "n_chunks", "table_bytes", "reserved")]
+
+
+class Matrix(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64), ("stride", C.c_int64),
+                ("type", C.c_int32), ("reserved", C.c_int32)]
+
+
+class Block8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("codes_stride", C.c_int64), ("scales_stride", C.c_int64), ("blocks", C.c_int32),
+                ("reserved", C.c_int32)]
 
 
 class AdamState(C.Structure):
@@ -159,7 +174,17 @@ def lib():
                                          C.c_int32, C.c_uint64, P, P]
     L.zero_mx8_encode.argtypes = [P, C.c_int64, C.c_int32, P, P, C.c_int32, C.c_uint64, C.c_int64, C.c_int64, P]
     L.zero_mx8_decode.argtypes = [P, P, C.c_int64, C.c_int32, P, P]
-    for name in ("zero_tensors_plan", "zero_tensors_grad_norm", "zero_tensors_adam_step", "zero_mx8_encode",
+    M, M8 = C.POINTER(Matrix), C.POINTER(Block8)
+    L.zero_block8_encode.argtypes = [M, P, P, C.c_int32, M8, M8, P]
+    L.zero_rms_norm8.argtypes = [M, M, P, C.c_int32, C.c_double, M, M8, P, P]
+    L.zero_rms_norm8_backward.argtypes = [M, M, P, C.c_int32, P, M, M, P, P, P]
+    L.zero_rms_norm8_workspace_bytes.argtypes = [C.c_int64, C.c_int64]
+    L.zero_block8_product.argtypes = [M8, M8, M, M, P, P]
+    L.zero_block8_workspace_bytes.argtypes = [C.c_int64, C.c_int64, C.c_int64]
+    for name in ("zero_rms_norm8_workspace_bytes", "zero_block8_workspace_bytes"):
+        getattr(L, name).restype = C.c_int64
+    for name in ("zero_block8_encode", "zero_rms_norm8", "zero_rms_norm8_backward", "zero_block8_product",
+                 "zero_tensors_plan", "zero_tensors_grad_norm", "zero_tensors_adam_step", "zero_mx8_encode",
                  "zero_mx8_decode", "zero_plan_partitions", "zero_memory_model", "zero_reduce_owned", "zero_adam_step",
                  "zero_adam_step_noalloc", "zero_calib_triad", "zero_calib_stream_mix", "zero_adam_step_buckets",
                  "zero_gather_layers", "zero_calib_slice_read",
@@ -691,6 +716,168 @@ def mx8_decode(codes, scales, x, root: bool = False, stream=None):
     n = _check_mx8(x, codes, scales)
     _check(lib().zero_mx8_decode(_ptr(codes), _ptr(scales), n, int(bool(root)), _ptr(x), _stream(stream)),
            "zero_mx8_decode")
+
+
+# ------------------------------------------------------- 8-bit layer operators
+def _matrix(t, what: str, cur: int) -> Matrix:
+    """The C struct of a 2-D device tensor whose rows are contiguous."""
+    kind = _LIST_TYPES.get(_dtype_name(t))
+    if kind is None:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected one of {tuple(_LIST_TYPES)}")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: a 2-D tensor expected, got {t.dim()} dimensions")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be neighbours")
+    if t.get_device() != cur:
+        _check_current(t, what, cur)
+    # the strides of a single row, or of no elements, have no meaning (torch may give any)
+    return Matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 and cols else cols, kind, 0)
+
+
+def _block8(codes, scales, what: str, cur: int, blocks: Optional[str] = None) -> Block8:
+    """The C struct of a matrix in the 8-bit form.  The kind of its blocks
+    follows from the scales' shape where it is not given (a single row has
+    the same scales in both)."""
+    if _dtype_name(codes) not in _CODES or _dtype_name(scales) not in _SCALES:
+        raise ValueError(f"{what}: codes of {_CODES} and scales of {_SCALES} expected, got {codes.dtype} and "
+                         f"{scales.dtype}")
+    if codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError(f"{what}: 2-D codes and scales expected")
+    rows, cols = codes.shape
+    across, down = -(-cols // BLOCK8), -(-rows // BLOCK8)
+    srows = int(scales.shape[0])
+    if scales.shape[1] != across or srows not in {"rows": (rows,), "tiles": (down,), None: (rows, down)}[blocks]:
+        raise ValueError(f"{what}: scales of {tuple(scales.shape)} for codes of {tuple(codes.shape)}, expected "
+                         f"({rows} or {down}, {across}) by rows or tiles")
+    if (cols > 1 and codes.stride(1) != 1) or (across > 1 and scales.stride(1) != 1):
+        raise ValueError(f"{what}: the bytes of a row must be neighbours")
+    for t in (codes, scales):
+        if t.get_device() != cur:
+            _check_current(t, what, cur)
+    kind = BLOCKS["rows" if srows == rows else "tiles"] if blocks is None else BLOCKS[blocks]
+    # the strides of a single row, or of no elements, have no meaning (torch may give any)
+    return Block8(codes.data_ptr(), scales.data_ptr(), rows, cols,
+                  codes.stride(0) if rows > 1 and cols else -(-cols // 16) * 16,
+                  scales.stride(0) if srows > 1 and cols else -(-across // 4) * 4, kind, 0)
+
+
+def _blocks(name: str) -> str:
+    if name not in BLOCKS:
+        raise ValueError(f"blocks: {name!r}, expected one of {tuple(BLOCKS)}")
+    return name
+
+
+def _vector(t, n: int, kinds: Sequence[str], what: str, cur: int) -> int:
+    if t.dim() != 1 or t.numel() != n:
+        raise ValueError(f"{what}: {n} elements expected, got a tensor of {tuple(t.shape)}")
+    _check_operand(t, n, tuple(kinds), what, cur)
+    return t.data_ptr()
+
+
+def _scratch(ws, need: int, what: str, cur: int) -> Optional[int]:
+    """The address of a workspace of at least ``need`` bytes (None for 0)."""
+    if need == 0:
+        return None
+    if ws is None or ws.numel() * ws.element_size() < need or not ws.is_contiguous():
+        raise ValueError(f"{what}: a contiguous device tensor of at least {need} bytes")
+    _check_current(ws, what, cur)
+    return ws.data_ptr()
+
+
+def _ref(x):
+    return None if x is None else C.byref(x)
+
+
+def block8_buffers(rows: int, cols: int, blocks: str = "rows", device=None):
+    """New (codes, scales) tensors for a matrix of rows x cols in the 8-bit
+    form, filled with zeros: views [rows, cols] and [rows or tiles of 128 rows,
+    blocks of 128 columns] of buffers whose rows are padded to 16 and 4 bytes,
+    as the calls want them."""
+    import torch
+    if rows < 0 or cols < 0:
+        raise ValueError(f"block8_buffers: {rows} x {cols}")
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    across = -(-cols // BLOCK8)
+    srows = rows if _blocks(blocks) == "rows" else -(-rows // BLOCK8)
+    codes = torch.zeros(rows, -(-cols // 16) * 16, dtype=torch.uint8, device=device)
+    scales = torch.zeros(srows, -(-across // 4) * 4, dtype=torch.uint8, device=device)
+    return (codes.view(torch.float8_e4m3fn)[:, :cols], scales.view(torch.float8_e8m0fnu)[:, :across])
+
+
+def block8_encode(x, codes=None, scales=None, codes_t=None, scales_t=None, blocks: str = "rows", row_mul=None,
+                  col_mul=None, stream=None):
+    """A float32, float16 or bfloat16 matrix, or x * row_mul[:, None] * col_mul,
+    into the 8-bit form: ``codes`` and ``scales`` as it is, ``codes_t`` and
+    ``scales_t`` transposed (either pair may be None).  ``blocks``: "rows" (128
+    values along a row of the codes share a scale) or "tiles" (128 x 128)."""
+    cur = _current_device()
+    _blocks(blocks)
+    mx = _matrix(x, "matrix", cur)
+    if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
+        raise ValueError("codes and scales come together")
+    out = None if codes is None else _block8(codes, scales, "codes", cur, blocks)
+    out_t = None if codes_t is None else _block8(codes_t, scales_t, "transposed codes", cur, blocks)
+    rm = None if row_mul is None else _vector(row_mul, mx.rows, ("float32",), "row multipliers", cur)
+    cm, ctype = None, TYPE_NONE
+    if col_mul is not None:
+        cm = _vector(col_mul, mx.cols, tuple(_LIST_TYPES), "column multipliers", cur)
+        ctype = _LIST_TYPES[_dtype_name(col_mul)]
+    _check(lib().zero_block8_encode(C.byref(mx), rm, cm, ctype, _ref(out), _ref(out_t), _stream(stream)),
+           "zero_block8_encode")
+
+
+def rms_norm8(x, weight, codes, scales, rstd, residual=None, h=None, eps: float = 1e-6, stream=None):
+    """The root-mean-square norm of x (+ residual) times ``weight``, in the 8-bit
+    form by rows.  ``rstd`` (float32 [rows]) and with a residual ``h`` (the sum, of
+    x's dtype; may be x or residual itself) are written for the backward pass."""
+    cur = _current_device()
+    mx = _matrix(x, "x", cur)
+    mr = None if residual is None else _matrix(residual, "residual", cur)
+    mh = None if h is None else _matrix(h, "h", cur)
+    w = _vector(weight, mx.cols, tuple(_LIST_TYPES), "weight", cur)
+    r = _vector(rstd, mx.rows, ("float32",), "rstd", cur)
+    _check(lib().zero_rms_norm8(C.byref(mx), _ref(mr), w, _LIST_TYPES[_dtype_name(weight)], float(eps), _ref(mh),
+                                C.byref(_block8(codes, scales, "codes", cur, "rows")), r, _stream(stream)),
+           "zero_rms_norm8")
+
+
+def rms_norm8_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().zero_rms_norm8_workspace_bytes(int(rows), int(cols)))
+
+
+def rms_norm8_backward(dy, h, weight, rstd, dx, dweight=None, workspace=None, dh=None, stream=None):
+    """rms_norm8's gradients: ``dx`` (of x and of residual; may be dy or dh
+    itself) and ``dweight`` (float32, or None).  ``h``: rms_norm8's h, or its x
+    where it had no residual.  ``dh``: what reaches h another way."""
+    cur = _current_device()
+    my, mh, mx = _matrix(dy, "dy", cur), _matrix(h, "h", cur), _matrix(dx, "dx", cur)
+    md = None if dh is None else _matrix(dh, "dh", cur)
+    w = _vector(weight, my.cols, tuple(_LIST_TYPES), "weight", cur)
+    r = _vector(rstd, my.rows, ("float32",), "rstd", cur)
+    dw = ws = None
+    if dweight is not None:
+        dw = _vector(dweight, my.cols, ("float32",), "dweight", cur)
+        ws = _scratch(workspace, rms_norm8_workspace_bytes(my.rows, my.cols), "workspace", cur)
+    _check(lib().zero_rms_norm8_backward(C.byref(my), C.byref(mh), w, _LIST_TYPES[_dtype_name(weight)], r, _ref(md),
+                                         C.byref(mx), dw, ws, _stream(stream)), "zero_rms_norm8_backward")
+
+
+def block8_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(lib().zero_block8_workspace_bytes(int(m), int(n), int(k)))
+
+
+def block8_product(a, a_scales, b, b_scales, out, add=None, workspace=None, stream=None):
+    """out = a b^T (+ add) of two matrices in the 8-bit form, [M, K] and [N, K].
+    ``add``: of out's dtype and shape; may be out itself.  ``workspace``: of
+    block8_workspace_bytes(M, N, K) bytes (may be None if that is 0)."""
+    cur = _current_device()
+    ma, mb = _block8(a, a_scales, "a", cur), _block8(b, b_scales, "b", cur)
+    mo = _matrix(out, "out", cur)
+    mc = None if add is None else _matrix(add, "add", cur)
+    ws = _scratch(workspace, block8_workspace_bytes(ma.rows, mb.rows, ma.cols), "workspace", cur)
+    _check(lib().zero_block8_product(C.byref(ma), C.byref(mb), _ref(mc), C.byref(mo), ws, _stream(stream)),
+           "zero_block8_product")
 
 
 # ------------------------------------------------------------------ calibration

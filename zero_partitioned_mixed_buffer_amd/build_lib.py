@@ -22,10 +22,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libzero_dp.so")
-HOST_SOURCES = ("zero_dp_host.cpp", "zero_dp_calls.cpp", "zero_dp_tensors.cpp")
+HOST_SOURCES = ("zero_dp_host.cpp", "zero_dp_calls.cpp", "zero_dp_tensors.cpp", "zero_dp_block8.cpp")
 # the step's kernels and launchers; the tensor-list operators'; the
-# benchmark's calibration kernels
-DEVICE_SOURCES = ("zero_dp_kernels.hip", "zero_dp_tensors.hip", "zero_dp_calib.hip")
+# 8-bit layer operators' (encode and norm; product); the benchmark's
+# calibration kernels
+DEVICE_SOURCES = ("zero_dp_kernels.hip", "zero_dp_tensors.hip", "zero_dp_block8.hip", "zero_dp_product.hip",
+                  "zero_dp_calib.hip")
 ARCH = "gfx950"
 
 HIP_FLAGS = [
@@ -69,7 +71,7 @@ def build(verbose: bool = False, asm: bool = False) -> str:
         _run([hipcc, *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", o], verbose)
         dev_objs.append(o)
     if asm:
-        for src in DEVICE_SOURCES[:2]:
+        for src in DEVICE_SOURCES[:-1]:
             _run([hipcc, *HIP_FLAGS, "-I", INCLUDE, "--cuda-device-only", "-S", os.path.join(CSRC, src), "-o",
                   os.path.join(BUILD, src.replace(".hip", ".s"))], verbose)
     tmp = LIB + ".tmp"

@@ -1,0 +1,123 @@
+// Internal declarations of the 8-bit layer operators (the encode of a
+// matrix, the root-mean-square norm and its gradients, the product of two
+// encoded matrices), shared by their host unit (zero_dp_block8.cpp) and their
+// device units (zero_dp_block8.hip, zero_dp_product.hip).  Not part of the
+// public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include "zero_dp_internal.h"
+
+namespace zdp {
+
+constexpr int kB8 = 128;                      // values that share a scale, along a row
+constexpr int64_t kB8MaxCols = 1 << 23;       // columns, and bytes between rows of codes
+constexpr int64_t kB8MaxRows = INT32_MAX;
+
+inline int64_t b8_blocks(int64_t n) { return (n + kB8 - 1) / kB8; }
+
+// Workgroups of the norm's backward pass, each with a row of partial sums of
+// dweight in the workspace: as many as there are rows, up to 1024 (four to a
+// CU), fewer for long rows, whose partial sums would fill memory (at most
+// 2^26 of them, but 64 rows).
+inline int64_t norm_back_groups(int64_t rows, int64_t cols) {
+    int64_t g = cols > 0 ? (INT64_C(1) << 26) / cols : 1024;
+    g = g > 1024 ? 1024 : g < 64 ? 64 : g;
+    return rows < g ? rows : g;
+}
+
+// Tiles of 256 x 256 that a product's launch may have (the runtime takes grids
+// of less than 2^32 lanes).
+constexpr int64_t kProductMaxTiles = 1 << 22;
+
+inline int64_t product_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256); }
+
+// Which of the product's kernels takes a size.
+enum ProductShape { kProductFew, kProductSmall, kProductLarge };
+
+inline ProductShape product_shape(int64_t m, int64_t n) {
+    if (m <= 64) return kProductFew;
+    return product_tiles(m, n) >= 128 ? kProductLarge : kProductSmall;
+}
+
+// Parts that a product's sum over k is split into (more than one: each part's
+// fp32 sums go to the workspace, and a second launch adds them up).
+inline int product_parts(int64_t m, int64_t n, int64_t k) {
+    if (product_shape(m, n) != kProductSmall) return 1;
+    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
+    int64_t parts = 512 / tiles;
+    const int64_t most = k / 1024;
+    parts = parts < most ? parts : most;
+    if (parts < 2) return 1;
+    // parts begin at a multiple of four blocks; none is empty
+    const int64_t blocks = b8_blocks(k), per = ((blocks + parts - 1) / parts + 3) / 4 * 4;
+    return static_cast<int>((blocks + per - 1) / per);
+}
+
+struct NormArgs {
+    const void* x;
+    const void* r;  // residual, or null
+    void* h;        // null without a residual
+    const void* w;
+    uint8_t* codes;
+    uint8_t* scales;
+    float* rstd;
+    int64_t rows, x_stride, r_stride, h_stride, codes_stride, scales_stride;
+    int32_t cols, type, w_type;
+    double eps;
+};
+
+struct NormBackArgs {
+    const void* dy;
+    const void* h;
+    const void* dh;  // or null
+    void* dx;
+    const void* w;
+    const float* rstd;
+    float* dw;       // or null
+    float* part;     // [norm_back_groups][cols]
+    int64_t rows, dy_stride, h_stride, dh_stride, dx_stride;
+    int32_t cols, type, w_type;
+};
+
+struct EncodeArgs {
+    const void* x;
+    const float* row_mul;  // or null
+    const void* col_mul;   // or null
+    uint8_t* codes;        // or null
+    uint8_t* scales;
+    uint8_t* codes_t;      // or null
+    uint8_t* scales_t;
+    int64_t rows, cols, x_stride, codes_stride, scales_stride, codes_t_stride, scales_t_stride;
+    int32_t type, col_type;
+    bool tiles;
+};
+
+// One operand of a product: scale row of code row r is r >> shift.
+struct ProductSide {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t rows;
+    uint32_t codes_stride;
+    int64_t scales_stride;
+    int32_t shift;
+};
+
+struct ProductArgs {
+    ProductSide a, b;
+    const void* add;  // or null
+    void* out;
+    float* part;      // [parts][m][n]
+    int64_t add_stride, out_stride;
+    int32_t k, type;
+};
+
+// Every argument has been validated by the caller, and no operand is empty
+// but k.  Each returns ZERO_OK or ZERO_EHIP.
+int launch_norm8(const NormArgs& a, void* stream);
+int launch_norm8_backward(const NormBackArgs& a, void* stream);
+int launch_block8_encode(const EncodeArgs& a, void* stream);
+int launch_block8_product(const ProductArgs& a, int parts, void* stream);
+
+}  // namespace zdp

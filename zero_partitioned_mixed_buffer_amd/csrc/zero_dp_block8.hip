@@ -1,0 +1,809 @@
+// Device side of the 8-bit layer operators for CDNA4 (gfx950): the encode of a
+// matrix, and the root-mean-square norm with its gradients.
+//
+//   norm      h = T(x + r);  rstd = 1 / sqrt(mean h^2 + eps);  y = (h rstd) w, in
+//             the 8-bit form by rows
+//   backward  xh = h rstd;  g = dy w;  c = mean(g xh);
+//             dx = (g - xh c) rstd + dh;  dw = sum over rows of dy xh
+//   encode    x, or x row_mul col_mul, in the 8-bit form, its transposed, or both
+//
+// All of it is a stream over memory: each input is read once and each output
+// written once.  A lane owns units of 8 consecutive columns (16 bytes of
+// 16-bit values, 8 of codes), so that the 16 lanes of a DPP row own one block
+// of 128 and its largest magnitude takes four register moves.  No two
+// workgroups write the same bytes and every sum has a fixed order, so results
+// repeat bit for bit.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/zero_dp.h"
+#include "zero_dp_block8.h"
+#include "zero_dp_fp8.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+using zdp::bits_of;
+using zdp::EncodeArgs;
+using zdp::float_of;
+using zdp::kB8;
+using zdp::NormArgs;
+using zdp::NormBackArgs;
+using zdp::scale_byte;
+
+constexpr int kU = 8;           // columns of a lane's unit
+constexpr int kSweep = 64 * kU;  // columns of a wave's sweep: four blocks
+
+// Rows and vectors need only their elements' own alignment.
+typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// ------------------------------------------------------ units of 8 elements
+template <int kType>
+struct Raw {
+    static constexpr int kWords = kType == ZERO_TYPE_F32 ? 8 : 4;
+    static constexpr int kSize = kType == ZERO_TYPE_F32 ? 4 : 2;
+    uint32_t w[kWords];
+};
+
+// Elements c .. c + 7 of a row of n; zeros past its end.
+template <int kType>
+__device__ __forceinline__ Raw<kType> load_unit(const char* row, int c, int n) {
+    Raw<kType> x;
+    if (c + kU <= n) {
+        if (kType == ZERO_TYPE_F32) {
+            const u32x4_4* p = reinterpret_cast<const u32x4_4*>(row + static_cast<int64_t>(c) * 4);
+            const u32x4_4 a = p[0], b = p[1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x.w[i] = a[i];
+                x.w[(4 + i) % Raw<kType>::kWords] = b[i];
+            }
+        } else {
+            const u32x4_2 a = *reinterpret_cast<const u32x4_2*>(row + static_cast<int64_t>(c) * 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.w[i] = a[i];
+        }
+        return x;
+    }
+#pragma unroll
+    for (int i = 0; i < Raw<kType>::kWords; ++i) x.w[i] = 0;
+    if (c >= n) return x;
+    if (kType == ZERO_TYPE_F32) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + c;
+#pragma unroll
+        for (int i = 0; i < Raw<kType>::kWords; ++i)
+            if (c + i < n) x.w[i] = p[i];
+    } else {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+            if (c + i < n) x.w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    }
+    return x;
+}
+
+template <int kType>
+__device__ __forceinline__ void store_unit(char* row, int c, int n, const Raw<kType>& x) {
+    if (c + kU <= n) {
+        if (kType == ZERO_TYPE_F32) {
+            u32x4_4 a, b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = x.w[i];
+                b[i] = x.w[(4 + i) % Raw<kType>::kWords];
+            }
+            u32x4_4* p = reinterpret_cast<u32x4_4*>(row + static_cast<int64_t>(c) * 4);
+            p[0] = a;
+            p[1] = b;
+        } else {
+            u32x4_2 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = x.w[i];
+            *reinterpret_cast<u32x4_2*>(row + static_cast<int64_t>(c) * 2) = a;
+        }
+        return;
+    }
+    if (kType == ZERO_TYPE_F32) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(row) + c;
+#pragma unroll
+        for (int i = 0; i < Raw<kType>::kWords; ++i)
+            if (c + i < n) p[i] = x.w[i];
+    } else {
+        uint16_t* p = reinterpret_cast<uint16_t*>(row) + c;
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+            if (c + i < n) p[i] = static_cast<uint16_t>(x.w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+template <int kType>
+__device__ __forceinline__ void unpack(const Raw<kType>& x, float (&v)[kU]) {
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+        if (kType == ZERO_TYPE_F32) {
+            v[i] = float_of(x.w[i % Raw<kType>::kWords]);
+        } else if (kType == ZERO_TYPE_BF16) {
+            v[i] = float_of(i & 1 ? x.w[i / 2] & 0xFFFF0000u : x.w[i / 2] << 16);
+        } else {
+            v[i] = static_cast<float>(__builtin_bit_cast(f16x2, x.w[i / 2])[i & 1]);
+        }
+    }
+}
+
+// To the type, to nearest even.
+template <int kType>
+__device__ __forceinline__ Raw<kType> pack(const float (&v)[kU]) {
+    Raw<kType> x;
+#pragma unroll
+    for (int i = 0; i < Raw<kType>::kWords; ++i) {
+        if (kType == ZERO_TYPE_F32) {
+            x.w[i] = bits_of(v[i]);
+        } else if (kType == ZERO_TYPE_BF16) {
+            bf16x2 t;
+            t[0] = static_cast<__bf16>(v[2 * i % kU]);
+            t[1] = static_cast<__bf16>(v[(2 * i + 1) % kU]);
+            x.w[i] = __builtin_bit_cast(uint32_t, t);
+        } else {
+            f16x2 t;
+            t[0] = static_cast<_Float16>(v[2 * i % kU]);
+            t[1] = static_cast<_Float16>(v[(2 * i + 1) % kU]);
+            x.w[i] = __builtin_bit_cast(uint32_t, t);
+        }
+    }
+    return x;
+}
+
+// A vector of any of the types (a norm's weight): the branch is the same for
+// the whole grid.
+__device__ __forceinline__ void load_vector(const void* w, int type, int c, int n, float (&v)[kU]) {
+    const char* p = static_cast<const char*>(w);
+    if (type == ZERO_TYPE_F32)
+        unpack(load_unit<ZERO_TYPE_F32>(p, c, n), v);
+    else if (type == ZERO_TYPE_F16)
+        unpack(load_unit<ZERO_TYPE_F16>(p, c, n), v);
+    else
+        unpack(load_unit<ZERO_TYPE_BF16>(p, c, n), v);
+}
+
+// ------------------------------------------------------------- reductions
+// Largest value over the 16 lanes of a DPP row.
+__device__ __forceinline__ uint32_t max16(uint32_t x) {
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xF, 0xF, true)));   // lane ^ 1
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xF, 0xF, true)));   // lane ^ 2
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x141, 0xF, 0xF, true)));  // other half of 8
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x140, 0xF, 0xF, true)));  // other half of 16
+    return x;
+}
+
+// Sum over a row's waves, the same in every lane.
+template <int kWaves, typename F>
+__device__ __forceinline__ F row_sum(F x) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    if (kWaves > 1) {
+        __shared__ F s[kWaves];
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = s[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) x += s[w];
+        __syncthreads();
+    }
+    return x;
+}
+
+// ------------------------------------------------------------------- codes
+__device__ __forceinline__ uint32_t magnitude(const float (&v)[kU]) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < kU; ++i) big = max(big, bits_of(v[i]) & 0x7FFFFFFFu);
+    return big;
+}
+
+// The codes of four values under their block's scale byte.  The largest
+// scale's codes end at 240: 256 * 2^120 would read as inf.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, uint32_t byte) {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    constexpr float most = 0x1.Ep127f;
+    const float scale = float_of(byte << 23);
+    a = __builtin_amdgcn_fmed3f(a, -most, most);
+    b = __builtin_amdgcn_fmed3f(b, -most, most);
+    c = __builtin_amdgcn_fmed3f(c, -most, most);
+    d = __builtin_amdgcn_fmed3f(d, -most, most);
+    s16x2 r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
+    return byte == 255u ? 0x7F7F7F7Fu : __builtin_bit_cast(uint32_t, r);
+}
+
+// A unit's codes; rows of codes start on 16 bytes.
+__device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, uint32_t lo, uint32_t hi) {
+    if (c + kU <= n) {
+        u32x2 x;
+        x[0] = lo;
+        x[1] = hi;
+        *reinterpret_cast<u32x2*>(row + c) = x;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+        if (c + i < n) row[c + i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+}
+
+// The scale bytes of a wave's sweep, whose first column is c0: one word, or
+// single bytes at the end of the row.
+__device__ __forceinline__ void store_scales(uint8_t* row, int c0, int n, uint32_t byte) {
+    const int lane = threadIdx.x & 63, b0 = c0 / kB8, nb = (n + kB8 - 1) / kB8;
+    uint32_t word = byte << (8 * (lane >> 4));
+    word |= __shfl_xor(word, 16);
+    word |= __shfl_xor(word, 32);
+    if (b0 + 4 <= nb) {
+        if (lane == 0) *reinterpret_cast<uint32_t*>(row + b0) = word;
+    } else if ((lane & 15) == 0 && b0 + (lane >> 4) < nb) {
+        row[b0 + (lane >> 4)] = static_cast<uint8_t>(byte);
+    }
+}
+
+// A unit of values, in the 8-bit form by rows.
+__device__ __forceinline__ void emit(uint8_t* codes, uint8_t* scales, int c, int n, const float (&v)[kU]) {
+    const uint32_t byte = scale_byte(max16(magnitude(v)));
+    store_codes(codes, c, n, codes4(v[0], v[1], v[2], v[3], byte), codes4(v[4], v[5], v[6], v[7], byte));
+    store_scales(scales, c & ~(kSweep - 1), n, byte);
+}
+
+template <int kType>
+__device__ __forceinline__ const char* row_of(const void* p, int64_t row, int64_t stride) {
+    return static_cast<const char*>(p) + row * stride * Raw<kType>::kSize;
+}
+template <int kType>
+__device__ __forceinline__ char* row_of(void* p, int64_t row, int64_t stride) {
+    return static_cast<char*>(p) + row * stride * Raw<kType>::kSize;
+}
+
+// h = T(x + r) of a unit: what is stored, and its values.
+template <int kType>
+__device__ __forceinline__ Raw<kType> add_units(const Raw<kType>& x, const Raw<kType>& r, float (&v)[kU]) {
+    float b[kU];
+    unpack(x, v);
+    unpack(r, b);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) v[i] += b[i];
+    const Raw<kType> h = pack<kType>(v);
+    unpack(h, v);
+    return h;
+}
+
+__device__ __forceinline__ double square_sum(const float (&v)[kU], double s) {
+#pragma unroll
+    for (int i = 0; i < kU; ++i) s = __builtin_fma(static_cast<double>(v[i]), static_cast<double>(v[i]), s);
+    return s;
+}
+
+__device__ __forceinline__ float rstd_of(double sum, int cols, double eps) {
+    return static_cast<float>(1.0 / __builtin_sqrt(sum / cols + eps));
+}
+
+__device__ __forceinline__ void scaled(const float (&h)[kU], float rstd, const float (&w)[kU], float (&y)[kU]) {
+#pragma unroll
+    for (int i = 0; i < kU; ++i) y[i] = (h[i] * rstd) * w[i];
+}
+
+// ------------------------------------------------------------------- norm
+// kWaves waves hold a row in registers, kNS units a lane.  Rows of one wave
+// need no barrier; four of them make a workgroup.
+template <int kWaves>
+constexpr int kThreads = kWaves == 1 ? 256 : 64 * kWaves;
+template <int kWaves>
+constexpr int kGroupRows = kWaves == 1 ? 4 : 1;
+
+template <int kType, bool kRes, int kWaves, int kNS>
+__global__ __launch_bounds__(kThreads<kWaves>) void norm8_kernel(NormArgs a) {
+    const int c0 = (kWaves == 1 ? threadIdx.x & 63 : threadIdx.x) * kU;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroupRows<kWaves>;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kGroupRows<kWaves> + (kWaves == 1 ? threadIdx.x >> 6 : 0);
+         row < a.rows; row += step) {
+        const char* x = row_of<kType>(a.x, row, a.x_stride);
+        const char* r = row_of<kType>(a.r, row, a.r_stride);
+        char* h = row_of<kType>(a.h, row, a.h_stride);
+        Raw<kType> rx[kNS], rr[kNS];
+        float v[kNS][kU];
+#pragma unroll
+        for (int s = 0; s < kNS; ++s) rx[s] = load_unit<kType>(x, c0 + s * kWaves * kSweep, a.cols);
+        if (kRes) {
+#pragma unroll
+            for (int s = 0; s < kNS; ++s) rr[s] = load_unit<kType>(r, c0 + s * kWaves * kSweep, a.cols);
+        }
+        double sum = 0.0;
+#pragma unroll
+        for (int s = 0; s < kNS; ++s) {
+            const int c = c0 + s * kWaves * kSweep;
+            if (kRes) {
+                const Raw<kType> y = add_units(rx[s], rr[s], v[s]);
+                if (c < a.cols) store_unit(h, c, a.cols, y);
+            } else {
+                unpack(rx[s], v[s]);
+            }
+            sum = square_sum(v[s], sum);
+        }
+        const float rstd = rstd_of(row_sum<kWaves>(sum), a.cols, a.eps);
+        if (c0 == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int s = 0; s < kNS; ++s) {
+            const int c = c0 + s * kWaves * kSweep;
+            if ((c & ~(kSweep - 1)) >= a.cols) break;  // the whole wave
+            float w[kU], y[kU];
+            load_vector(a.w, a.w_type, c, a.cols, w);
+            scaled(v[s], rstd, w, y);
+            emit(a.codes + row * a.codes_stride, a.scales + row * a.scales_stride, c, a.cols, y);
+        }
+    }
+}
+
+// Rows longer than the registers of a workgroup: read twice (h again, out of
+// the cache; each lane reads what it wrote itself).
+constexpr int kLongWaves = 16;
+
+template <int kType, bool kRes>
+__global__ __launch_bounds__(kLongWaves * 64) void norm8_long_kernel(NormArgs a) {
+    constexpr int kStep = kLongWaves * kSweep;
+    const int c0 = threadIdx.x * kU;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const char* x = row_of<kType>(a.x, row, a.x_stride);
+        const char* r = row_of<kType>(a.r, row, a.r_stride);
+        char* h = row_of<kType>(a.h, row, a.h_stride);
+        double sum = 0.0;
+        for (int c = c0; c < a.cols; c += kStep) {
+            float v[kU];
+            const Raw<kType> rx = load_unit<kType>(x, c, a.cols);
+            if (kRes)
+                store_unit(h, c, a.cols, add_units(rx, load_unit<kType>(r, c, a.cols), v));
+            else
+                unpack(rx, v);
+            sum = square_sum(v, sum);
+        }
+        const float rstd = rstd_of(row_sum<kLongWaves>(sum), a.cols, a.eps);
+        if (threadIdx.x == 0) a.rstd[row] = rstd;
+        for (int c = c0; (c & ~(kSweep - 1)) < a.cols; c += kStep) {
+            float v[kU], w[kU], y[kU];
+            unpack(load_unit<kType>(kRes ? h : x, c, a.cols), v);
+            load_vector(a.w, a.w_type, c, a.cols, w);
+            scaled(v, rstd, w, y);
+            emit(a.codes + row * a.codes_stride, a.scales + row * a.scales_stride, c, a.cols, y);
+        }
+    }
+}
+
+// --------------------------------------------------------------- backward
+// A unit's xh and g = dy w.
+__device__ __forceinline__ void parts_of(const float (&dy)[kU], const float (&h)[kU], const float (&w)[kU], float rstd,
+                                         float (&g)[kU], float (&xh)[kU]) {
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+        xh[i] = h[i] * rstd;
+        g[i] = dy[i] * w[i];
+    }
+}
+
+template <int kType>
+__device__ __forceinline__ Raw<kType> grad_unit(const float (&g)[kU], const float (&xh)[kU], float c, float rstd,
+                                                bool has_dh, const Raw<kType>& dh) {
+    float v[kU], d[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) v[i] = (g[i] - xh[i] * c) * rstd;
+    if (has_dh) {
+        unpack(dh, d);
+#pragma unroll
+        for (int i = 0; i < kU; ++i) v[i] += d[i];
+    }
+    return pack<kType>(v);
+}
+
+// Each workgroup takes rows in turn and keeps its part of dweight in
+// registers, one row of `part` at the end.
+template <int kType, int kWaves, int kNS>
+__global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBackArgs a) {
+    const int c0 = (kWaves == 1 ? threadIdx.x & 63 : threadIdx.x) * kU;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroupRows<kWaves>;
+    const bool has_dh = a.dh != nullptr;
+    float dw[kNS][kU];
+#pragma unroll
+    for (int s = 0; s < kNS; ++s)
+#pragma unroll
+        for (int i = 0; i < kU; ++i) dw[s][i] = 0.0f;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kGroupRows<kWaves> + (kWaves == 1 ? threadIdx.x >> 6 : 0);
+         row < a.rows; row += step) {
+        const float rstd = a.rstd[row];
+        Raw<kType> ry[kNS], rh[kNS], rd[kNS];
+#pragma unroll
+        for (int s = 0; s < kNS; ++s) {
+            const int c = c0 + s * kWaves * kSweep;
+            ry[s] = load_unit<kType>(row_of<kType>(a.dy, row, a.dy_stride), c, a.cols);
+            rh[s] = load_unit<kType>(row_of<kType>(a.h, row, a.h_stride), c, a.cols);
+            if (has_dh) rd[s] = load_unit<kType>(row_of<kType>(a.dh, row, a.dh_stride), c, a.cols);
+        }
+        float g[kNS][kU], xh[kNS][kU], sum = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kNS; ++s) {
+            float dy[kU], h[kU], w[kU];
+            load_vector(a.w, a.w_type, c0 + s * kWaves * kSweep, a.cols, w);
+            unpack(ry[s], dy);
+            unpack(rh[s], h);
+            parts_of(dy, h, w, rstd, g[s], xh[s]);
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                sum += g[s][i] * xh[s][i];
+                dw[s][i] += dy[i] * xh[s][i];
+            }
+        }
+        const float c = row_sum<kWaves>(sum) / static_cast<float>(a.cols);
+#pragma unroll
+        for (int s = 0; s < kNS; ++s) {
+            const int at = c0 + s * kWaves * kSweep;
+            if (at < a.cols)
+                store_unit(row_of<kType>(a.dx, row, a.dx_stride), at, a.cols,
+                           grad_unit<kType>(g[s], xh[s], c, rstd, has_dh, rd[s]));
+        }
+    }
+    if (a.dw == nullptr) return;
+    float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
+    if (kWaves == 1) {
+        __shared__ float all[4][kNS * kSweep];
+#pragma unroll
+        for (int s = 0; s < kNS; ++s)
+#pragma unroll
+            for (int i = 0; i < kU; ++i) all[threadIdx.x >> 6][s * kSweep + c0 + i] = dw[s][i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.cols; c += 256) part[c] = (all[0][c] + all[1][c]) + (all[2][c] + all[3][c]);
+        return;
+    }
+#pragma unroll
+    for (int s = 0; s < kNS; ++s) {
+        const int c = c0 + s * kWaves * kSweep;
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+            if (c + i < a.cols) part[c + i] = dw[s][i];
+    }
+}
+
+// Rows longer than the registers of a workgroup: dy and h read twice, and the
+// workgroup's part of dweight summed up in memory (each lane its own columns).
+template <int kType>
+__global__ __launch_bounds__(kLongWaves * 64) void norm8_backward_long_kernel(NormBackArgs a) {
+    constexpr int kStep = kLongWaves * kSweep;
+    const int c0 = threadIdx.x * kU;
+    const bool has_dh = a.dh != nullptr;
+    float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
+    bool first = true;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
+        const float rstd = a.rstd[row];
+        const char* dy_row = row_of<kType>(a.dy, row, a.dy_stride);
+        const char* h_row = row_of<kType>(a.h, row, a.h_stride);
+        float sum = 0.0f;
+        for (int c = c0; c < a.cols; c += kStep) {
+            float dy[kU], h[kU], w[kU], g[kU], xh[kU];
+            unpack(load_unit<kType>(dy_row, c, a.cols), dy);
+            unpack(load_unit<kType>(h_row, c, a.cols), h);
+            load_vector(a.w, a.w_type, c, a.cols, w);
+            parts_of(dy, h, w, rstd, g, xh);
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                sum += g[i] * xh[i];
+                if (a.dw != nullptr && c + i < a.cols) part[c + i] = (first ? 0.0f : part[c + i]) + dy[i] * xh[i];
+            }
+        }
+        const float mean = row_sum<kLongWaves>(sum) / static_cast<float>(a.cols);
+        for (int c = c0; c < a.cols; c += kStep) {
+            float dy[kU], h[kU], w[kU], g[kU], xh[kU];
+            Raw<kType> rd = {};
+            unpack(load_unit<kType>(dy_row, c, a.cols), dy);
+            unpack(load_unit<kType>(h_row, c, a.cols), h);
+            load_vector(a.w, a.w_type, c, a.cols, w);
+            if (has_dh) rd = load_unit<kType>(row_of<kType>(a.dh, row, a.dh_stride), c, a.cols);
+            parts_of(dy, h, w, rstd, g, xh);
+            store_unit(row_of<kType>(a.dx, row, a.dx_stride), c, a.cols,
+                       grad_unit<kType>(g, xh, mean, rstd, has_dh, rd));
+        }
+    }
+}
+
+// dweight = the parts' sum, in float64 and a fixed order: 16 columns and 64
+// parts at a time to a workgroup.
+__global__ __launch_bounds__(1024) void norm8_dweight_kernel(const float* part, int groups, int cols, float* dw) {
+    __shared__ double s[64][17];
+    const int j = threadIdx.x & 15, g0 = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + j;
+    double x = 0.0;
+    if (c < cols)
+        for (int g = g0; g < groups; g += 64) x += part[static_cast<int64_t>(g) * cols + c];
+    s[g0][j] = x;
+    __syncthreads();
+    if (threadIdx.x >= 16 || c >= cols) return;
+    x = 0.0;
+    for (int g = 0; g < 64; ++g) x += s[g][j];
+    dw[c] = static_cast<float>(x);
+}
+
+// ----------------------------------------------------------------- encode
+template <bool kMul>
+__device__ __forceinline__ void multiply(const EncodeArgs& a, int64_t row, const float (&w)[kU], float (&v)[kU]) {
+    if (!kMul) return;
+    const float m = a.row_mul != nullptr ? a.row_mul[row] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < kU; ++i) v[i] = (v[i] * m) * w[i];
+}
+
+template <bool kMul>
+__device__ __forceinline__ void multipliers(const EncodeArgs& a, int c, float (&w)[kU]) {
+    if (kMul && a.col_mul != nullptr) {
+        load_vector(a.col_mul, a.col_type, c, static_cast<int>(a.cols), w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) w[i] = 1.0f;
+    }
+}
+
+// By rows, as it is: a wave takes sweeps of 512 columns.
+template <int kType, bool kMul>
+__global__ __launch_bounds__(256) void encode_rows_kernel(EncodeArgs a) {
+    const int cols = static_cast<int>(a.cols);
+    const int sweeps = (cols + kSweep - 1) / kSweep;
+    const int64_t units = a.rows * sweeps;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); u < units;
+         u += static_cast<int64_t>(gridDim.x) * 4) {
+        const int64_t row = u / sweeps;
+        const int c = static_cast<int>(u - row * sweeps) * kSweep + (threadIdx.x & 63) * kU;
+        float v[kU], w[kU];
+        unpack(load_unit<kType>(row_of<kType>(a.x, row, a.x_stride), c, cols), v);
+        multipliers<kMul>(a, c, w);
+        multiply<kMul>(a, row, w, v);
+        emit(a.codes + row * a.codes_stride, a.scales + row * a.scales_stride, c, cols, v);
+    }
+}
+
+// 128 x 128 values to a workgroup: lane group g (16 lanes) holds rows 8 g to
+// 8 g + 7, each lane 8 columns of them.  Transposed codes go through LDS,
+// where a lane's 8 rows of a column are 8 neighbouring bytes.
+constexpr int kTurnStride = 144;
+
+template <int kType, bool kMul, bool kTiles>
+__global__ __launch_bounds__(256) void encode_tile_kernel(EncodeArgs a) {
+    __shared__ uint32_t top[4][kB8];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kB8 * kTurnStride];
+    const int cols = static_cast<int>(a.cols);
+    const int across = (cols + kB8 - 1) / kB8;
+    const int64_t tiles = (a.rows + kB8 - 1) / kB8 * across;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t tr = tile / across, r0 = tr * kB8 + rg * 8;
+        const int tc = static_cast<int>(tile - tr * across), c = tc * kB8 + cg * kU;
+        Raw<kType> raw[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = r0 + j < a.rows;
+            raw[j] = load_unit<kType>(row_of<kType>(a.x, in ? r0 + j : 0, a.x_stride), c, in ? cols : 0);
+        }
+        float w[kU], v[8][kU];
+        multipliers<kMul>(a, c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            unpack(raw[j], v[j]);
+            if (r0 + j < a.rows) multiply<kMul>(a, r0 + j, w, v[j]);
+        }
+        uint32_t tile_byte = 0;
+        if (kTiles) {
+            uint32_t big = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) big = max(big, magnitude(v[j]));
+            big = max16(big);
+            big = max(big, static_cast<uint32_t>(__shfl_xor(big, 16)));
+            big = max(big, static_cast<uint32_t>(__shfl_xor(big, 32)));
+            if ((threadIdx.x & 63) == 0) top[wave][0] = big;
+            __syncthreads();
+            tile_byte = scale_byte(max(max(top[0][0], top[1][0]), max(top[2][0], top[3][0])));
+            if (threadIdx.x == 0) {
+                if (a.codes != nullptr) a.scales[tr * a.scales_stride + tc] = static_cast<uint8_t>(tile_byte);
+                if (a.codes_t != nullptr) a.scales_t[tc * a.scales_t_stride + tr] = static_cast<uint8_t>(tile_byte);
+            }
+        }
+        if (a.codes != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t byte = kTiles ? tile_byte : scale_byte(max16(magnitude(v[j])));
+                const int64_t row = r0 + j;
+                if (row >= a.rows) continue;
+                if (c < cols)
+                    store_codes(a.codes + row * a.codes_stride, c, cols,
+                                codes4(v[j][0], v[j][1], v[j][2], v[j][3], byte),
+                                codes4(v[j][4], v[j][5], v[j][6], v[j][7], byte));
+                if (!kTiles && cg == 0) a.scales[row * a.scales_stride + tc] = static_cast<uint8_t>(byte);
+            }
+        }
+        if (a.codes_t != nullptr) {
+            uint32_t big[kU];
+            if (!kTiles) {
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    uint32_t x = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x = max(x, bits_of(v[j][i]) & 0x7FFFFFFFu);
+                    x = max(x, static_cast<uint32_t>(__shfl_xor(x, 16)));
+                    x = max(x, static_cast<uint32_t>(__shfl_xor(x, 32)));
+                    if ((threadIdx.x & 48) == 0) top[wave][cg * kU + i] = x;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    const int k = cg * kU + i;
+                    big[i] = max(max(top[0][k], top[1][k]), max(top[2][k], top[3][k]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                const uint32_t byte = kTiles ? tile_byte : scale_byte(big[i]);
+                u32x2 x;
+                x[0] = codes4(v[0][i], v[1][i], v[2][i], v[3][i], byte);
+                x[1] = codes4(v[4][i], v[5][i], v[6][i], v[7][i], byte);
+                *reinterpret_cast<u32x2*>(turned + (cg * kU + i) * kTurnStride + rg * 8) = x;
+                if (!kTiles && rg == 0 && c + i < cols)
+                    a.scales_t[static_cast<int64_t>(c + i) * a.scales_t_stride + tr] = static_cast<uint8_t>(byte);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int k = p * 32 + (threadIdx.x >> 3), part = (threadIdx.x & 7) * 16;
+                const int64_t col = static_cast<int64_t>(tc) * kB8 + k, r = tr * kB8 + part;
+                if (col >= cols || r >= a.rows) continue;
+                const u32x4 x = *reinterpret_cast<const u32x4*>(turned + k * kTurnStride + part);
+                uint8_t* to = a.codes_t + col * a.codes_t_stride + r;
+                if (r + 16 <= a.rows) {
+                    *reinterpret_cast<u32x4*>(to) = x;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (r + i < a.rows) to[i] = static_cast<uint8_t>(x[i / 4] >> (8 * (i & 3)));
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// --------------------------------------------------------------- launchers
+// Grids are capped far below the runtime's limit of 2^32 lanes; the kernels
+// take what is left in turn.
+constexpr int64_t kMaxGrid = 1 << 20;
+
+unsigned grid_of(int64_t units) { return static_cast<unsigned>(units < kMaxGrid ? units : kMaxGrid); }
+
+int finish() {
+    const hipError_t e = hipGetLastError();
+    if (e == hipSuccess) return ZERO_OK;
+    zdp::set_last_hip_error(static_cast<int>(e));
+    return ZERO_EHIP;
+}
+
+// Calls f with the type as a constant.
+template <typename F>
+void with_type(int type, F f) {
+    if (type == ZERO_TYPE_F32)
+        f(std::integral_constant<int, ZERO_TYPE_F32>());
+    else if (type == ZERO_TYPE_F16)
+        f(std::integral_constant<int, ZERO_TYPE_F16>());
+    else
+        f(std::integral_constant<int, ZERO_TYPE_BF16>());
+}
+
+// Calls f with the waves and the units a lane that hold a row of n columns:
+// (0, 0) for a row too long for registers.
+template <typename F>
+void with_row_shape(int n, F f) {
+    using std::integral_constant;
+    if (n <= kSweep)
+        f(integral_constant<int, 1>(), integral_constant<int, 1>());
+    else if (n <= 2 * kSweep)
+        f(integral_constant<int, 1>(), integral_constant<int, 2>());
+    else if (n <= 4 * kSweep)
+        f(integral_constant<int, 1>(), integral_constant<int, 4>());
+    else if (n <= 8 * kSweep)
+        f(integral_constant<int, 4>(), integral_constant<int, 2>());
+    else if (n <= 16 * kSweep)
+        f(integral_constant<int, 4>(), integral_constant<int, 4>());
+    else if (n <= 32 * kSweep)
+        f(integral_constant<int, 16>(), integral_constant<int, 2>());
+    else
+        f(integral_constant<int, 0>(), integral_constant<int, 0>());
+}
+
+}  // namespace
+
+namespace zdp {
+
+int launch_norm8(const NormArgs& a, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    with_type(a.type, [&](auto type) {
+        constexpr int kType = decltype(type)::value;
+        with_row_shape(a.cols, [&](auto waves, auto units) {
+            constexpr int kWaves = decltype(waves)::value, kNS = decltype(units)::value;
+            if constexpr (kWaves == 0) {
+                const unsigned grid = grid_of(a.rows);
+                if (a.r != nullptr)
+                    norm8_long_kernel<kType, true><<<grid, kLongWaves * 64, 0, s>>>(a);
+                else
+                    norm8_long_kernel<kType, false><<<grid, kLongWaves * 64, 0, s>>>(a);
+            } else {
+                const unsigned grid = grid_of((a.rows - 1) / kGroupRows<kWaves> + 1);
+                if (a.r != nullptr)
+                    norm8_kernel<kType, true, kWaves, kNS><<<grid, kThreads<kWaves>, 0, s>>>(a);
+                else
+                    norm8_kernel<kType, false, kWaves, kNS><<<grid, kThreads<kWaves>, 0, s>>>(a);
+            }
+        });
+    });
+    return finish();
+}
+
+int launch_norm8_backward(const NormBackArgs& a, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    int64_t groups = norm_back_groups(a.rows, a.cols);
+    if (a.rows > 0) {
+        with_type(a.type, [&](auto type) {
+            constexpr int kType = decltype(type)::value;
+            with_row_shape(a.cols, [&](auto waves, auto units) {
+                constexpr int kWaves = decltype(waves)::value, kNS = decltype(units)::value;
+                if constexpr (kWaves == 0) {
+                    norm8_backward_long_kernel<kType><<<static_cast<unsigned>(groups), kLongWaves * 64, 0, s>>>(a);
+                } else {
+                    const int64_t most = (a.rows - 1) / kGroupRows<kWaves> + 1;
+                    groups = groups < most ? groups : most;
+                    norm8_backward_kernel<kType, kWaves, kNS>
+                        <<<static_cast<unsigned>(groups), kThreads<kWaves>, 0, s>>>(a);
+                }
+            });
+        });
+        const int rc = finish();
+        if (rc != ZERO_OK) return rc;
+    }
+    if (a.dw == nullptr) return ZERO_OK;
+    norm8_dweight_kernel<<<static_cast<unsigned>((a.cols + 15) / 16), 1024, 0, s>>>(
+        a.part, a.rows > 0 ? static_cast<int>(groups) : 0, a.cols, a.dw);
+    return finish();
+}
+
+int launch_block8_encode(const EncodeArgs& a, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool mul = a.row_mul != nullptr || a.col_mul != nullptr;
+    with_type(a.type, [&](auto type) {
+        constexpr int kType = decltype(type)::value;
+        if (!a.tiles && a.codes_t == nullptr) {
+            const unsigned grid = grid_of((a.rows * ((a.cols + kSweep - 1) / kSweep) + 3) / 4);
+            if (mul)
+                encode_rows_kernel<kType, true><<<grid, 256, 0, s>>>(a);
+            else
+                encode_rows_kernel<kType, false><<<grid, 256, 0, s>>>(a);
+            return;
+        }
+        const unsigned grid = grid_of(b8_blocks(a.rows) * b8_blocks(a.cols));
+        if (a.tiles) {
+            if (mul)
+                encode_tile_kernel<kType, true, true><<<grid, 256, 0, s>>>(a);
+            else
+                encode_tile_kernel<kType, false, true><<<grid, 256, 0, s>>>(a);
+        } else {
+            if (mul)
+                encode_tile_kernel<kType, true, false><<<grid, 256, 0, s>>>(a);
+            else
+                encode_tile_kernel<kType, false, false><<<grid, 256, 0, s>>>(a);
+        }
+    });
+    return finish();
+}
+
+}  // namespace zdp

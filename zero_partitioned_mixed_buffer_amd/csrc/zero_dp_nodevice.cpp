@@ -4,6 +4,7 @@
 // undefined-behaviour sanitizers.  Every launch reports ZERO_EHIP with
 // hipErrorNoDevice (100), so a call that passes validation fails loudly;
 // nothing here computes anything.
+#include "zero_dp_block8.h"
 #include "zero_dp_calib.h"
 #include "zero_dp_internal.h"
 #include "zero_dp_tensors.h"
@@ -51,5 +52,9 @@ int launch_mx8_encode(const float*, int64_t, bool, uint8_t*, uint8_t*, bool, uin
     return no_device();
 }
 int launch_mx8_decode(const uint8_t*, const uint8_t*, int64_t, bool, float*, void*) { return no_device(); }
+int launch_norm8(const NormArgs&, void*) { return no_device(); }
+int launch_norm8_backward(const NormBackArgs&, void*) { return no_device(); }
+int launch_block8_encode(const EncodeArgs&, void*) { return no_device(); }
+int launch_block8_product(const ProductArgs&, int, void*) { return no_device(); }
 
 }  // namespace zdp

@@ -1,0 +1,496 @@
+// Device side of the product of two matrices in the 8-bit form, for CDNA4
+// (gfx950):  out[m][n] = T(sum_k a[m][k] b[n][k] + add[m][n]).
+//
+// Scales are powers of two, one for 128 values along k, so the scaled matrix
+// instructions (32x32x64 and 16x16x128, one scale byte a lane and operand)
+// take them as they are: the sum over k stays in the accumulators from the
+// first block to the last, with no arithmetic beside the instructions.  The
+// hardware adds the products of neighbouring k after aligning them to the
+// largest, with 14 bits below it; what is cut off is far less than the 8-bit
+// codes' own rounding and than a 16-bit output's, but not than fp32's.  fp32
+// outputs therefore widen the codes to bf16 (exact, the scale with them) and
+// take the bf16 instructions, at half the rate.
+//
+// The order in which an instruction takes its k does not matter as long as
+// both operands have the same, which leaves the layouts in LDS free.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/zero_dp.h"
+#include "zero_dp_block8.h"
+#include "zero_dp_fp8.h"
+
+namespace {
+
+using zdp::kB8;
+using zdp::ProductArgs;
+using zdp::ProductSide;
+using zdp::scale_value;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32_1 __attribute__((aligned(1)));
+
+// ----------------------------------------------------------------- outputs
+template <int kType>
+struct Out;
+template <>
+struct Out<ZERO_TYPE_F32> {
+    typedef float T;
+};
+template <>
+struct Out<ZERO_TYPE_F16> {
+    typedef _Float16 T;
+};
+template <>
+struct Out<ZERO_TYPE_BF16> {
+    typedef __bf16 T;
+};
+
+// kN neighbouring elements of a row, of which the first `left` are there; the
+// row is aligned to its elements only.
+template <typename T, int kN>
+struct Pack {
+    typedef T V __attribute__((ext_vector_type(kN), aligned(sizeof(T))));
+};
+
+template <typename T, int kN>
+__device__ __forceinline__ void store_run(T* to, const float (&v)[kN], const T* add, int64_t left) {
+    typedef typename Pack<T, kN>::V V;
+    if (left >= kN) {
+        V x;
+        if (add != nullptr) {
+            const V y = *reinterpret_cast<const V*>(add);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) x[i] = static_cast<T>(v[i] + static_cast<float>(y[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) x[i] = static_cast<T>(v[i]);
+        }
+        *reinterpret_cast<V*>(to) = x;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (i < left) to[i] = static_cast<T>(v[i] + (add != nullptr ? static_cast<float>(add[i]) : 0.0f));
+}
+
+// ------------------------------------------------------------------- codes
+// 16 codes of which the first `left` count, the others zero.
+__device__ __forceinline__ i32x4 keep(i32x4 x, int left) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int b = left - 4 * i;
+        x[i] = b >= 4 ? x[i] : b <= 0 ? 0 : x[i] & static_cast<int>((1u << (8 * b)) - 1u);
+    }
+    return x;
+}
+
+__device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) { return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+
+// Eight codes (two words) as bf16 under a scale; exact from 2^-126 up.
+__device__ __forceinline__ bf16x8 widen(int lo, int hi, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Codes under the scale byte 255 are NaN, whatever they are.
+__device__ __forceinline__ int poisoned(int word, uint32_t byte) { return byte == 255u ? 0x7F7F7F7F : word; }
+
+__device__ __forceinline__ const uint8_t* scale_row(const ProductSide& s, int64_t row) {
+    return s.scales + (row >> s.shift) * s.scales_stride;
+}
+
+// ------------------------------------------------------------------- tiles
+// A workgroup computes kBM x kBN of out with kWM x kWN waves, each of them
+// kFM x kFN squares of 32.  Blocks of 128 k of both operands go to LDS
+// through direct loads (16 bytes a lane, no registers), the next block's
+// under way while this one's are multiplied.
+//
+// In LDS a row's 128 bytes are eight pieces of 16, piece q of row p at place
+// q ^ (p / 2 % 8): the 16 or 32 rows that a read takes at one piece then lie
+// in different banks.  b's rows are dealt to LDS so that the kFN squares of
+// a lane hold neighbouring columns of out, which it stores at once.
+template <int kBM_, int kBN_, int kWM_, int kWN_>
+struct Shape {
+    static constexpr int kBM = kBM_, kBN = kBN_, kWM = kWM_, kWN = kWN_;
+    static constexpr int kThreads = 64 * kWM * kWN;
+    static constexpr int kFM = kBM / kWM / 32, kFN = kBN / kWN / 32;
+    static constexpr int kStage = (kBM + kBN) * kB8;
+    static constexpr int kLoadsA = kBM * 8 / kThreads, kLoadsB = kBN * 8 / kThreads;
+    static_assert(kThreads % 128 == 0 && kBM * 8 % kThreads == 0 && kBN * 8 % kThreads == 0, "whole loads");
+};
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+__device__ __forceinline__ int place(int p, int q) { return p * kB8 + ((q ^ (p >> 1 & 7)) << 4); }
+
+template <typename S, int kType, bool kExact>
+__global__ __launch_bounds__(S::kThreads, 1) void product_kernel(ProductArgs a, int parts) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S::kStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / S::kWN, wn = wave % S::kWN;
+
+    // Consecutive workgroups go to the eight dies in turn; each die takes a
+    // run of neighbouring tiles, whose operands then meet in its L2.
+    const int64_t tm = (a.a.rows + S::kBM - 1) / S::kBM, tn = (a.b.rows + S::kBN - 1) / S::kBN;
+    const int64_t tiles = tm * tn;
+    const int part = blockIdx.y;
+    int64_t id;
+    {
+        const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3, q = tiles >> 3, r = tiles & 7;
+        id = x * q + (x < r ? x : r) + i;
+    }
+    // ... in bands of 8 tile rows, column by column
+    const int64_t band = id / (8 * tn), in_band = id - band * 8 * tn;
+    const int64_t high = tm - band * 8 < 8 ? tm - band * 8 : 8;
+    const int64_t m0 = (band * 8 + in_band % high) * S::kBM, n0 = in_band / high * S::kBN;
+
+    const int blocks = (a.k + kB8 - 1) / kB8;
+    // parts begin at a multiple of four blocks (a word of scales)
+    const int per = ((blocks + parts - 1) / parts + 3) & ~3;
+    const int first = part * per, last = first + per < blocks ? first + per : blocks;
+
+    // Rows past the end repeat the last one (their results are not stored).
+    const uint8_t* const base_a = a.a.codes + m0 * a.a.codes_stride;
+    const uint8_t* const base_b = a.b.codes + n0 * a.b.codes_stride;
+    const int rows_a = a.a.rows - m0 < S::kBM ? static_cast<int>(a.a.rows - m0) : S::kBM;
+    const int rows_b = a.b.rows - n0 < S::kBN ? static_cast<int>(a.b.rows - n0) : S::kBN;
+    uint32_t off_a[S::kLoadsA], off_b[S::kLoadsB];
+    // the piece of its row that a lane loads, the same in all its rows (they are a multiple of 16 apart)
+    const uint32_t piece = static_cast<uint32_t>((lane & 7) ^ (threadIdx.x >> 4 & 7)) << 4;
+#pragma unroll
+    for (int i = 0; i < S::kLoadsA; ++i) {
+        const int p = (i * S::kThreads + static_cast<int>(threadIdx.x)) >> 3;
+        const int row = p < rows_a ? p : rows_a - 1;
+        off_a[i] = static_cast<uint32_t>(row) * a.a.codes_stride + piece;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kLoadsB; ++i) {
+        const int p = (i * S::kThreads + static_cast<int>(threadIdx.x)) >> 3;
+        const int w = p / (32 * S::kFN), f = p / 32 % S::kFN, c = p & 31;
+        const int n = w * 32 * S::kFN + c * S::kFN + f;
+        const int row = n < rows_b ? n : rows_b - 1;
+        off_b[i] = static_cast<uint32_t>(row) * a.b.codes_stride + piece;
+    }
+    const auto load = [&](int block, int stage) {
+        const uint32_t k0 = static_cast<uint32_t>(block) * kB8;
+        // bytes of the block's pieces that lie in the row; pieces past its end repeat the block's first
+        const uint32_t in = (static_cast<uint32_t>(a.k) - k0 + 15) & ~15u;
+        const uint32_t back = piece >= in ? piece : 0;
+        uint8_t* const to = lds + stage * S::kStage + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < S::kLoadsA; ++i) {
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(base_a + k0 + (off_a[i] - back)),
+                (lds_ptr)(to + i * S::kThreads * 16), 16, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < S::kLoadsB; ++i) {
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(base_b + k0 + (off_b[i] - back)),
+                (lds_ptr)(to + S::kBM * kB8 + i * S::kThreads * 16), 16, 0, 0);
+        }
+    };
+
+    // Scales of the lane's rows: one word holds four blocks.
+    const uint8_t *sa[S::kFM], *sb[S::kFN];
+    const int r32 = lane & 31, g = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < S::kFM; ++i) {
+        const int p = wm * 32 * S::kFM + i * 32 + r32;
+        sa[i] = scale_row(a.a, m0 + (p < rows_a ? p : rows_a - 1));
+    }
+#pragma unroll
+    for (int j = 0; j < S::kFN; ++j) {
+        const int n = wn * 32 * S::kFN + r32 * S::kFN + j;
+        sb[j] = scale_row(a.b, n0 + (n < rows_b ? n : rows_b - 1));
+    }
+    uint32_t wa[S::kFM], wb[S::kFN];
+
+    f32x16 acc[S::kFM][S::kFN];
+#pragma unroll
+    for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::kFN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    const auto multiply = [&](int block, int stage, auto tail) {
+        constexpr bool kTail = decltype(tail)::value;
+        const uint8_t* const at_a = lds + stage * S::kStage;
+        const uint8_t* const at_b = at_a + S::kBM * kB8;
+        const int left = a.k - block * kB8;  // codes of the row that are left
+        const int shift = 8 * (block & 3);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            i32x8 fa[S::kFM], fb[S::kFN];
+            const int q0 = kk * 4 + g * 2;
+#pragma unroll
+            for (int i = 0; i < S::kFM; ++i) {
+                const int p = wm * 32 * S::kFM + i * 32 + r32;
+                i32x4 x = *reinterpret_cast<const i32x4*>(at_a + place(p, q0));
+                i32x4 y = *reinterpret_cast<const i32x4*>(at_a + place(p, q0 + 1));
+                if (kTail) {
+                    x = keep(x, left - q0 * 16);
+                    y = keep(y, left - q0 * 16 - 16);
+                }
+                fa[i] = join(x, y);
+            }
+#pragma unroll
+            for (int j = 0; j < S::kFN; ++j) {
+                const int p = wn * 32 * S::kFN + j * 32 + r32;
+                i32x4 x = *reinterpret_cast<const i32x4*>(at_b + place(p, q0));
+                i32x4 y = *reinterpret_cast<const i32x4*>(at_b + place(p, q0 + 1));
+                if (kTail) {
+                    x = keep(x, left - q0 * 16);
+                    y = keep(y, left - q0 * 16 - 16);
+                }
+                fb[j] = join(x, y);
+            }
+            if (!kExact) {
+#pragma unroll
+                for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::kFN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            fa[i], fb[j], acc[i][j], 0, 0, 0, static_cast<int>(wa[i] >> shift), 0,
+                            static_cast<int>(wb[j] >> shift));
+            } else {
+                bf16x8 hb[S::kFN][4];
+#pragma unroll
+                for (int j = 0; j < S::kFN; ++j) {
+                    const uint32_t byte = wb[j] >> shift & 255u;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        hb[j][t] = widen(poisoned(fb[j][2 * t], byte), fb[j][2 * t + 1], scale_value(byte));
+                }
+#pragma unroll
+                for (int i = 0; i < S::kFM; ++i) {
+                    const uint32_t byte = wa[i] >> shift & 255u;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const bf16x8 ha = widen(poisoned(fa[i][2 * t], byte), fa[i][2 * t + 1], scale_value(byte));
+#pragma unroll
+                        for (int j = 0; j < S::kFN; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ha, hb[j][t], acc[i][j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    };
+
+    if (first < last) {
+        load(first, 0);
+        __syncthreads();
+        for (int block = first; block < last; ++block) {
+            const int stage = (block - first) & 1;
+            if (block + 1 < last) load(block + 1, stage ^ 1);
+            if ((block & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < S::kFM; ++i) wa[i] = *reinterpret_cast<const uint32_t*>(sa[i] + block);
+#pragma unroll
+                for (int j = 0; j < S::kFN; ++j) wb[j] = *reinterpret_cast<const uint32_t*>(sb[j] + block);
+            }
+            if ((block + 1) * kB8 <= a.k)
+                multiply(block, stage, std::false_type());
+            else
+                multiply(block, stage, std::true_type());
+            __syncthreads();
+        }
+    }
+
+    // A lane has kFN neighbouring columns of 16 rows of each of its squares.
+    const int col = wn * 32 * S::kFN + r32 * S::kFN;
+    const int64_t left = a.b.rows - n0 - col;
+    if (left <= 0) return;
+#pragma unroll
+    for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int p = wm * 32 * S::kFM + i * 32 + (e >> 2) * 8 + g * 4 + (e & 3);
+            if (p >= rows_a) continue;
+            float v[S::kFN];
+#pragma unroll
+            for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
+            const int64_t row = m0 + p;
+            if (parts > 1) {
+                float* to = a.part + (part * a.a.rows + row) * a.b.rows + n0 + col;
+                store_run<float, S::kFN>(to, v, nullptr, left);
+            } else {
+                typedef typename Out<kType>::T T;
+                T* to = static_cast<T*>(a.out) + row * a.out_stride + n0 + col;
+                const T* add = a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + n0 + col;
+                store_run<T, S::kFN>(to, v, add, left);
+            }
+        }
+}
+
+// The parts' sum, in order, and the addend.
+template <int kType>
+__global__ __launch_bounds__(256) void join_parts_kernel(ProductArgs a, int parts) {
+    typedef typename Out<kType>::T T;
+    const int64_t m = a.a.rows, n = a.b.rows, across = (n + 3) / 4;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < m * across;
+         u += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = u / across, c = (u - row * across) * 4;
+        const int left = n - c < 4 ? static_cast<int>(n - c) : 4;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int p = 0; p < parts; ++p) {
+            const float* from = a.part + (p * m + row) * n + c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) v[i] += from[i];
+        }
+        store_run<T, 4>(static_cast<T*>(a.out) + row * a.out_stride + c, v,
+                        a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + c, left);
+    }
+}
+
+// --------------------------------------------------------------- few rows
+// At most 64 rows of a (tokens), 16 kT of them: the time goes into reading b
+// once.  A workgroup takes 16 rows of b, its waves blocks of k in turn,
+// straight into registers; the waves' sums meet in LDS.  b is the
+// instruction's first operand, so that a lane holds four neighbouring columns
+// of out for one token.
+constexpr int kFewWaves = 8;
+
+template <int kType, bool kExact, int kT>
+__global__ __launch_bounds__(kFewWaves * 64) void product_few_kernel(ProductArgs a) {
+    __shared__ f32x4 sums[kFewWaves][kT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t row_b = n0 + r < a.b.rows ? n0 + r : a.b.rows - 1;
+    const uint8_t* const pb = a.b.codes + row_b * a.b.codes_stride;
+    const uint8_t* const sb = scale_row(a.b, row_b);
+    const uint8_t *pa[kT], *sa[kT];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+        const int64_t row = t * 16 + r < a.a.rows ? t * 16 + r : a.a.rows - 1;
+        pa[t] = a.a.codes + row * a.a.codes_stride;
+        sa[t] = scale_row(a.a, row);
+    }
+    f32x4 acc[kT];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int blocks = (a.k + kB8 - 1) / kB8;
+    for (int block = wave; block < blocks; block += kFewWaves) {
+        const int k = block * kB8 + g * 32, left = a.k - k;
+        // pieces past the row's end repeat its first
+        const int o0 = left > 0 ? k : 0, o1 = left > 16 ? k + 16 : 0;
+        i32x4 x = *reinterpret_cast<const i32x4*>(pb + o0), y = *reinterpret_cast<const i32x4*>(pb + o1);
+        const uint32_t eb = sb[block];
+        const i32x8 fb = join(keep(x, left), keep(y, left - 16));
+        i32x8 fa[kT];
+        uint32_t ea[kT];
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            x = *reinterpret_cast<const i32x4*>(pa[t] + o0);
+            y = *reinterpret_cast<const i32x4*>(pa[t] + o1);
+            fa[t] = join(keep(x, left), keep(y, left - 16));
+            ea[t] = sa[t][block];
+        }
+        if (!kExact) {
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa[t], acc[t], 0, 0, 0,
+                                                                          static_cast<int>(eb), 0,
+                                                                          static_cast<int>(ea[t]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bf16x8 hb = widen(poisoned(fb[2 * j], eb), fb[2 * j + 1], scale_value(eb));
+#pragma unroll
+                for (int t = 0; t < kT; ++t)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        hb, widen(poisoned(fa[t][2 * j], ea[t]), fa[t][2 * j + 1], scale_value(ea[t])), acc[t], 0, 0, 0);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t) sums[wave][t][lane] = acc[t];
+    __syncthreads();
+    if (wave >= kT) return;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+        const f32x4 x = sums[w][wave][lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += x[i];
+    }
+    const int64_t row = wave * 16 + r, c = n0 + g * 4;
+    if (row >= a.a.rows || c >= a.b.rows) return;
+    typedef typename Out<kType>::T T;
+    store_run<T, 4>(static_cast<T*>(a.out) + row * a.out_stride + c, v,
+                    a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + c, a.b.rows - c);
+}
+
+// --------------------------------------------------------------- launchers
+int finish() {
+    const hipError_t e = hipGetLastError();
+    if (e == hipSuccess) return ZERO_OK;
+    zdp::set_last_hip_error(static_cast<int>(e));
+    return ZERO_EHIP;
+}
+
+template <typename S, int kType>
+void launch_tiles(const ProductArgs& a, int parts, hipStream_t s) {
+    constexpr bool kExact = kType == ZERO_TYPE_F32;
+    const int64_t tiles = ((a.a.rows + S::kBM - 1) / S::kBM) * ((a.b.rows + S::kBN - 1) / S::kBN);
+    product_kernel<S, kType, kExact>
+        <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(parts)), S::kThreads, 0, s>>>(a, parts);
+    if (parts > 1) {
+        const int64_t units = (a.a.rows * ((a.b.rows + 3) / 4) + 255) / 256;
+        join_parts_kernel<kType><<<static_cast<unsigned>(units < 8192 ? units : 8192), 256, 0, s>>>(a, parts);
+    }
+}
+
+template <int kType>
+void launch_few(const ProductArgs& a, hipStream_t s) {
+    constexpr bool kExact = kType == ZERO_TYPE_F32;
+    const unsigned grid = static_cast<unsigned>((a.b.rows + 15) / 16);
+    if (a.a.rows <= 16)
+        product_few_kernel<kType, kExact, 1><<<grid, kFewWaves * 64, 0, s>>>(a);
+    else if (a.a.rows <= 32)
+        product_few_kernel<kType, kExact, 2><<<grid, kFewWaves * 64, 0, s>>>(a);
+    else
+        product_few_kernel<kType, kExact, 4><<<grid, kFewWaves * 64, 0, s>>>(a);
+}
+
+typedef Shape<256, 256, 2, 4> Large;
+typedef Shape<128, 128, 2, 2> Small;
+
+template <int kType>
+void launch_typed(const ProductArgs& a, int parts, hipStream_t s) {
+    switch (zdp::product_shape(a.a.rows, a.b.rows)) {
+        case zdp::kProductFew: launch_few<kType>(a, s); break;
+        case zdp::kProductSmall: launch_tiles<Small, kType>(a, parts, s); break;
+        default: launch_tiles<Large, kType>(a, parts, s); break;
+    }
+}
+
+}  // namespace
+
+namespace zdp {
+
+int launch_block8_product(const ProductArgs& a, int parts, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (a.type == ZERO_TYPE_F32)
+        launch_typed<ZERO_TYPE_F32>(a, parts, s);
+    else if (a.type == ZERO_TYPE_F16)
+        launch_typed<ZERO_TYPE_F16>(a, parts, s);
+    else
+        launch_typed<ZERO_TYPE_BF16>(a, parts, s);
+    return finish();
+}
+
+}  // namespace zdp

@@ -30,18 +30,23 @@
 #include <cstdint>
 
 #include "../../include/zero_dp.h"
+#include "zero_dp_fp8.h"
 #include "zero_dp_tensors.h"
 
 #pragma clang fp contract(off)
 
 namespace {
 
+using zdp::bits_of;
 using zdp::ChunkRef;
+using zdp::float_of;
 using zdp::kBlock;
 using zdp::kChunk;
 using zdp::kWaves;
 using zdp::ListArgs;
 using zdp::Partials;
+using zdp::scale_byte;
+using zdp::scale_value;
 using zdp::TensorDesc;
 using zdp::TensorStepArgs;
 
@@ -153,20 +158,6 @@ __host__ __device__ __forceinline__ RandomKey random_key(uint64_t seed, uint32_t
 __device__ __forceinline__ uint32_t random_word(const RandomKey& k, uint32_t c) { return mix(c ^ k.k1, k.k2); }
 
 // ------------------------------------------------------------ 8-bit blocks
-// Scale byte of a block whose largest magnitude has the bits `big`: the
-// exponent, one more where the mantissa passes 448 = 1.75 * 2^8.  255 for a
-// block that holds an inf or a NaN.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t big) {
-    int e = static_cast<int>((big + 0x1FFFFFu) >> 23) - 8;
-    e = e < 1 ? 1 : e;
-    return big >= 0x7F800000u ? 255u : static_cast<uint32_t>(e);
-}
-
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-    const uint32_t bits = byte == 255u ? 0x7FC00000u : byte == 0u ? 0x00400000u : byte << 23;
-    return __builtin_bit_cast(float, bits);
-}
-
 __device__ __forceinline__ fvec decode4(uint32_t codes, float scale) {
     const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), false);
     const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(codes), true);
@@ -177,9 +168,6 @@ __device__ __forceinline__ fvec decode4(uint32_t codes, float scale) {
     r[3] = b[1] * scale;
     return r;
 }
-
-__device__ __forceinline__ uint32_t bits_of(float x) { return __builtin_bit_cast(uint32_t, x); }
-__device__ __forceinline__ float float_of(uint32_t x) { return __builtin_bit_cast(float, x); }
 
 // Correctly rounded square roots of four fp32 values.  The hardware's root s
 // is off by at most one step u; x lies above the midpoint (s - u/2)^2 =
