@@ -648,8 +648,8 @@ typedef struct zero_matrix {
 
 /* rows x cols codes and their scales, device memory.  codes: 16-byte aligned,
  * codes_stride (bytes) >= cols, a multiple of 16 and at most 2^23.  scales:
- * 4-byte aligned, scales_stride (bytes) >= ceil(cols / 128), a multiple of 4.
- * cols <= 2^23, rows < 2^31. */
+ * 4-byte aligned, scales_stride (bytes) >= ceil(cols / 128), a multiple of 4
+ * and at most 2^23.  cols <= 2^23, rows < 2^31. */
 typedef struct zero_block8 {
     uint8_t* codes;
     uint8_t* scales;

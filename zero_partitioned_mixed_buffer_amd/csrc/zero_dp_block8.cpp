@@ -70,7 +70,9 @@ int check_block8(const zero_block8* m, int64_t rows, int64_t cols, Region* codes
         return ZERO_EINVAL;
     if (m->rows < 0 || m->cols < 0 || m->codes_stride < m->cols || m->scales_stride < 0) return ZERO_EINVAL;
     if ((rows >= 0 && m->rows != rows) || (cols >= 0 && m->cols != cols)) return ZERO_EINVAL;
-    if (m->rows > kB8MaxRows || m->cols > kB8MaxCols || m->codes_stride > kB8MaxCols) return ZERO_EOVERFLOW;
+    if (m->rows > kB8MaxRows || m->cols > kB8MaxCols || m->codes_stride > kB8MaxCols ||
+        m->scales_stride > kB8MaxCols)
+        return ZERO_EOVERFLOW;
     if (m->scales_stride < b8_blocks(m->cols)) return ZERO_EINVAL;
     if (m->codes_stride % 16 != 0 || m->scales_stride % 4 != 0) return ZERO_EALIGN;
     const int64_t srows = m->blocks == ZERO_BLOCK8_TILES ? b8_blocks(m->rows) : m->rows;

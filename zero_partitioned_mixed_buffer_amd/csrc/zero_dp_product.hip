@@ -112,110 +112,194 @@ __device__ __forceinline__ const uint8_t* scale_row(const ProductSide& s, int64_
 
 // ------------------------------------------------------------------- tiles
 // A workgroup computes kBM x kBN of out with kWM x kWN waves, each of them
-// kFM x kFN squares of 32.  Blocks of 128 k of both operands go to LDS
-// through direct loads (16 bytes a lane, no registers), the next block's
-// under way while this one's are multiplied.
+// kFM x kFN squares of 32.  Blocks of 128 k of both operands go to one of two
+// places in LDS through direct loads (16 bytes a lane, no registers), and from
+// there to registers, half a block at a time.  Everything is one step ahead
+// of the matrix instructions:
+//
+//   first half of block b:   multiply it; read b's second half
+//   barrier                  (b is in registers now, b + 1 is in LDS)
+//   second half of block b:  load b + 2 over b; read b + 1's first half; multiply
+//
+// so that a block has a whole block's time to come out of memory, a read half
+// a block's, and there is one barrier for 128 k.  Scales go the same way, four
+// blocks in a word of a row.
 //
 // In LDS a row's 128 bytes are eight pieces of 16, piece q of row p at place
-// q ^ (p / 2 % 8): the 16 or 32 rows that a read takes at one piece then lie
-// in different banks.  b's rows are dealt to LDS so that the kFN squares of
-// a lane hold neighbouring columns of out, which it stores at once.
+// q ^ (p / 2 % 8): the rows that a read takes at one piece lie in different
+// banks.  b's rows are dealt to LDS so that the kFN squares of a lane hold
+// neighbouring columns of out, which it stores at once.
 template <int kBM_, int kBN_, int kWM_, int kWN_>
 struct Shape {
     static constexpr int kBM = kBM_, kBN = kBN_, kWM = kWM_, kWN = kWN_;
     static constexpr int kThreads = 64 * kWM * kWN;
     static constexpr int kFM = kBM / kWM / 32, kFN = kBN / kWN / 32;
-    static constexpr int kStage = (kBM + kBN) * kB8;
+    static constexpr int kRows = kBM + kBN;
     static constexpr int kLoadsA = kBM * 8 / kThreads, kLoadsB = kBN * 8 / kThreads;
     static_assert(kThreads % 128 == 0 && kBM * 8 % kThreads == 0 && kBN * 8 % kThreads == 0, "whole loads");
+    static constexpr int kScalesA = (kBM + kThreads - 1) / kThreads, kScalesB = (kBN + kThreads - 1) / kThreads;
+    static constexpr int kReads = 2 * (kFM + kFN);  // LDS reads of a half block
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+__device__ __forceinline__ rsrc_t buffer_of(const uint8_t* p) {
+    // offsets are kept in bounds by construction
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0xFFFFFFFFu, 0x00027000);
+}
 
 __device__ __forceinline__ int place(int p, int q) { return p * kB8 + ((q ^ (p >> 1 & 7)) << 4); }
 
+// Asks the compiler to deal a half block's LDS reads out among its matrix
+// instructions, and to keep them on this side of what follows.
+template <typename S, bool kExact>
+__device__ __forceinline__ void interleave() {
+    if (!kExact) {
+#pragma unroll
+        for (int i = 0; i < S::kFM * S::kFN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);    // a matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x100, (S::kReads + S::kFM * S::kFN - 1) / (S::kFM * S::kFN), 0);  // reads
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Waits for this wave's LDS reads and direct loads, then for the workgroup.
+__device__ __forceinline__ void arrive() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <typename S, int kType, bool kExact>
-__global__ __launch_bounds__(S::kThreads, 1) void product_kernel(ProductArgs a, int parts) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S::kStage];
+__global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int parts) {
+    // two objects, so that the compiler sees that loads into one do not touch reads of the other
+    __shared__ __attribute__((aligned(1024))) uint8_t even[S::kRows * kB8];
+    __shared__ __attribute__((aligned(1024))) uint8_t odd[S::kRows * kB8];
+    __shared__ uint32_t lds_scales[2][S::kRows];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::kWN, wn = wave % S::kWN;
 
     // Consecutive workgroups go to the eight dies in turn; each die takes a
-    // run of neighbouring tiles, whose operands then meet in its L2.
-    const int64_t tm = (a.a.rows + S::kBM - 1) / S::kBM, tn = (a.b.rows + S::kBN - 1) / S::kBN;
-    const int64_t tiles = tm * tn;
-    const int part = blockIdx.y;
-    int64_t id;
-    {
-        const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3, q = tiles >> 3, r = tiles & 7;
-        id = x * q + (x < r ? x : r) + i;
-    }
+    // run of neighbouring tiles, whose operands then meet in its L2 ...
+    const uint32_t tm = static_cast<uint32_t>((a.a.rows + S::kBM - 1) / S::kBM);
+    const uint32_t tn = static_cast<uint32_t>((a.b.rows + S::kBN - 1) / S::kBN);
+    const uint32_t tiles = tm * tn, die = blockIdx.x & 7, rest = tiles & 7;
+    const uint32_t id = die * (tiles >> 3) + (die < rest ? die : rest) + (blockIdx.x >> 3);
     // ... in bands of 8 tile rows, column by column
-    const int64_t band = id / (8 * tn), in_band = id - band * 8 * tn;
-    const int64_t high = tm - band * 8 < 8 ? tm - band * 8 : 8;
-    const int64_t m0 = (band * 8 + in_band % high) * S::kBM, n0 = in_band / high * S::kBN;
+    const uint32_t band = id / (8 * tn), in_band = id - band * 8 * tn;
+    const uint32_t high = tm - band * 8 < 8 ? tm - band * 8 : 8;
+    const uint32_t across = in_band / high;
+    const int64_t m0 = static_cast<int64_t>(band * 8 + in_band - across * high) * S::kBM;
+    const int64_t n0 = static_cast<int64_t>(across) * S::kBN;
 
     const int blocks = (a.k + kB8 - 1) / kB8;
     // parts begin at a multiple of four blocks (a word of scales)
-    const int per = ((blocks + parts - 1) / parts + 3) & ~3;
+    const int part = blockIdx.y, per = ((blocks + parts - 1) / parts + 3) & ~3;
     const int first = part * per, last = first + per < blocks ? first + per : blocks;
 
     // Rows past the end repeat the last one (their results are not stored).
-    const uint8_t* const base_a = a.a.codes + m0 * a.a.codes_stride;
-    const uint8_t* const base_b = a.b.codes + n0 * a.b.codes_stride;
+    const rsrc_t codes_a = buffer_of(a.a.codes + m0 * a.a.codes_stride);
+    const rsrc_t codes_b = buffer_of(a.b.codes + n0 * a.b.codes_stride);
     const int rows_a = a.a.rows - m0 < S::kBM ? static_cast<int>(a.a.rows - m0) : S::kBM;
     const int rows_b = a.b.rows - n0 < S::kBN ? static_cast<int>(a.b.rows - n0) : S::kBN;
+    const auto row_of_a = [&](int p) { return p < rows_a ? p : rows_a - 1; };
+    const auto row_of_b = [&](int p) {
+        const int w = p / (32 * S::kFN), f = p / 32 % S::kFN, n = w * 32 * S::kFN + (p & 31) * S::kFN + f;
+        return n < rows_b ? n : rows_b - 1;
+    };
     uint32_t off_a[S::kLoadsA], off_b[S::kLoadsB];
     // the piece of its row that a lane loads, the same in all its rows (they are a multiple of 16 apart)
     const uint32_t piece = static_cast<uint32_t>((lane & 7) ^ (threadIdx.x >> 4 & 7)) << 4;
 #pragma unroll
-    for (int i = 0; i < S::kLoadsA; ++i) {
-        const int p = (i * S::kThreads + static_cast<int>(threadIdx.x)) >> 3;
-        const int row = p < rows_a ? p : rows_a - 1;
-        off_a[i] = static_cast<uint32_t>(row) * a.a.codes_stride + piece;
-    }
+    for (int i = 0; i < S::kLoadsA; ++i)
+        off_a[i] = static_cast<uint32_t>(row_of_a((i * S::kThreads + static_cast<int>(threadIdx.x)) >> 3)) *
+                       a.a.codes_stride + piece;
 #pragma unroll
-    for (int i = 0; i < S::kLoadsB; ++i) {
-        const int p = (i * S::kThreads + static_cast<int>(threadIdx.x)) >> 3;
-        const int w = p / (32 * S::kFN), f = p / 32 % S::kFN, c = p & 31;
-        const int n = w * 32 * S::kFN + c * S::kFN + f;
-        const int row = n < rows_b ? n : rows_b - 1;
-        off_b[i] = static_cast<uint32_t>(row) * a.b.codes_stride + piece;
-    }
-    const auto load = [&](int block, int stage) {
+    for (int i = 0; i < S::kLoadsB; ++i)
+        off_b[i] = static_cast<uint32_t>(row_of_b((i * S::kThreads + static_cast<int>(threadIdx.x)) >> 3)) *
+                       a.b.codes_stride + piece;
+
+    // Loads a block; pieces past the row's end repeat the block's first.
+    const auto load = [&](int block, auto slot) {
         const uint32_t k0 = static_cast<uint32_t>(block) * kB8;
-        // bytes of the block's pieces that lie in the row; pieces past its end repeat the block's first
         const uint32_t in = (static_cast<uint32_t>(a.k) - k0 + 15) & ~15u;
         const uint32_t back = piece >= in ? piece : 0;
-        uint8_t* const to = lds + stage * S::kStage + wave * 1024;
+        uint8_t* const to = (decltype(slot)::value ? odd : even) + wave * 1024;
 #pragma unroll
-        for (int i = 0; i < S::kLoadsA; ++i) {
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(base_a + k0 + (off_a[i] - back)),
-                (lds_ptr)(to + i * S::kThreads * 16), 16, 0, 0);
-        }
+        for (int i = 0; i < S::kLoadsA; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(codes_a, (lds_ptr)(to + i * S::kThreads * 16), 16,
+                                                     static_cast<int>(off_a[i] - back), static_cast<int>(k0), 0, 0);
 #pragma unroll
-        for (int i = 0; i < S::kLoadsB; ++i) {
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(base_b + k0 + (off_b[i] - back)),
-                (lds_ptr)(to + S::kBM * kB8 + i * S::kThreads * 16), 16, 0, 0);
+        for (int i = 0; i < S::kLoadsB; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(codes_b, (lds_ptr)(to + S::kBM * kB8 + i * S::kThreads * 16), 16,
+                                                     static_cast<int>(off_b[i] - back), static_cast<int>(k0), 0, 0);
+    };
+    // Loads the scales of four blocks; a wave's rows are all a's or all b's.
+    const rsrc_t scales_a = buffer_of(scale_row(a.a, m0)), scales_b = buffer_of(scale_row(a.b, n0));
+    uint32_t off_sa[S::kScalesA], off_sb[S::kScalesB];
+#pragma unroll
+    for (int i = 0; i < S::kScalesA; ++i)
+        off_sa[i] = static_cast<uint32_t>(row_of_a(i * S::kThreads + static_cast<int>(threadIdx.x)) >> a.a.shift) *
+                    static_cast<uint32_t>(a.a.scales_stride);
+#pragma unroll
+    for (int i = 0; i < S::kScalesB; ++i)
+        off_sb[i] = static_cast<uint32_t>(row_of_b(i * S::kThreads + static_cast<int>(threadIdx.x)) >> a.b.shift) *
+                    static_cast<uint32_t>(a.b.scales_stride);
+    const auto load_scales = [&](int block) {
+        uint32_t* const to = lds_scales[block >> 2 & 1] + wave * 64;
+#pragma unroll
+        for (int i = 0; i < S::kScalesA; ++i)
+            if ((i + 1) * S::kThreads <= S::kBM || i * S::kThreads + wave * 64 < S::kBM)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(scales_a, (lds_ptr)(to + i * S::kThreads), 4,
+                                                         static_cast<int>(off_sa[i]), block, 0, 0);
+#pragma unroll
+        for (int i = 0; i < S::kScalesB; ++i)
+            if ((i + 1) * S::kThreads <= S::kBN || i * S::kThreads + wave * 64 < S::kBN)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(scales_b, (lds_ptr)(to + S::kBM + i * S::kThreads), 4,
+                                                         static_cast<int>(off_sb[i]), block, 0, 0);
+    };
+    // Makes the codes past the row's end zeros.
+    const auto trim = [&](int block, uint8_t* at) {
+        const int left = a.k - block * kB8;
+        for (int u = threadIdx.x; u < S::kRows * 8; u += S::kThreads) {
+            const int p = u >> 3, q = u & 7;
+            if (q * 16 + 16 <= left) continue;
+            i32x4* const x = reinterpret_cast<i32x4*>(at + place(p, q));
+            *x = keep(*x, left - q * 16);
         }
+        arrive();
     };
 
-    // Scales of the lane's rows: one word holds four blocks.
-    const uint8_t *sa[S::kFM], *sb[S::kFN];
     const int r32 = lane & 31, g = lane >> 5;
-#pragma unroll
-    for (int i = 0; i < S::kFM; ++i) {
-        const int p = wm * 32 * S::kFM + i * 32 + r32;
-        sa[i] = scale_row(a.a, m0 + (p < rows_a ? p : rows_a - 1));
-    }
-#pragma unroll
-    for (int j = 0; j < S::kFN; ++j) {
-        const int n = wn * 32 * S::kFN + r32 * S::kFN + j;
-        sb[j] = scale_row(a.b, n0 + (n < rows_b ? n : rows_b - 1));
-    }
+    i32x8 fa[2][S::kFM], fb[2][S::kFN];
     uint32_t wa[S::kFM], wb[S::kFN];
+    const auto read_at = [&](const uint8_t* at, auto half) {
+        constexpr int kk = decltype(half)::value;
+        const int q = kk * 4 + g * 2;
+#pragma unroll
+        for (int i = 0; i < S::kFM; ++i) {
+            const int p = wm * 32 * S::kFM + i * 32 + r32;
+            fa[kk][i] = join(*reinterpret_cast<const i32x4*>(at + place(p, q)),
+                             *reinterpret_cast<const i32x4*>(at + place(p, q + 1)));
+        }
+#pragma unroll
+        for (int j = 0; j < S::kFN; ++j) {
+            const int p = S::kBM + wn * 32 * S::kFN + j * 32 + r32;
+            fb[kk][j] = join(*reinterpret_cast<const i32x4*>(at + place(p, q)),
+                             *reinterpret_cast<const i32x4*>(at + place(p, q + 1)));
+        }
+    };
+    const auto read = [&](auto slot, auto half) { read_at(decltype(slot)::value ? odd : even, half); };
+    const auto read_scales = [&](int block) {
+        const uint32_t* const at = lds_scales[block >> 2 & 1];
+        const int shift = 8 * (block & 3);
+#pragma unroll
+        for (int i = 0; i < S::kFM; ++i) wa[i] = at[wm * 32 * S::kFM + i * 32 + r32] >> shift;
+#pragma unroll
+        for (int j = 0; j < S::kFN; ++j) wb[j] = at[S::kBM + wn * 32 * S::kFN + j * 32 + r32] >> shift;
+    };
 
     f32x16 acc[S::kFM][S::kFN];
 #pragma unroll
@@ -225,88 +309,80 @@ __global__ __launch_bounds__(S::kThreads, 1) void product_kernel(ProductArgs a, 
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    const auto multiply = [&](int block, int stage, auto tail) {
-        constexpr bool kTail = decltype(tail)::value;
-        const uint8_t* const at_a = lds + stage * S::kStage;
-        const uint8_t* const at_b = at_a + S::kBM * kB8;
-        const int left = a.k - block * kB8;  // codes of the row that are left
-        const int shift = 8 * (block & 3);
+    const auto multiply = [&](auto half) {
+        constexpr int kk = decltype(half)::value;
+        if (!kExact) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            i32x8 fa[S::kFM], fb[S::kFN];
-            const int q0 = kk * 4 + g * 2;
+            for (int i = 0; i < S::kFM; ++i)
 #pragma unroll
-            for (int i = 0; i < S::kFM; ++i) {
-                const int p = wm * 32 * S::kFM + i * 32 + r32;
-                i32x4 x = *reinterpret_cast<const i32x4*>(at_a + place(p, q0));
-                i32x4 y = *reinterpret_cast<const i32x4*>(at_a + place(p, q0 + 1));
-                if (kTail) {
-                    x = keep(x, left - q0 * 16);
-                    y = keep(y, left - q0 * 16 - 16);
-                }
-                fa[i] = join(x, y);
-            }
+                for (int j = 0; j < S::kFN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        fa[kk][i], fb[kk][j], acc[i][j], 0, 0, 0, static_cast<int>(wa[i]), 0, static_cast<int>(wb[j]));
+        } else {
+            bf16x8 hb[S::kFN][4];
 #pragma unroll
             for (int j = 0; j < S::kFN; ++j) {
-                const int p = wn * 32 * S::kFN + j * 32 + r32;
-                i32x4 x = *reinterpret_cast<const i32x4*>(at_b + place(p, q0));
-                i32x4 y = *reinterpret_cast<const i32x4*>(at_b + place(p, q0 + 1));
-                if (kTail) {
-                    x = keep(x, left - q0 * 16);
-                    y = keep(y, left - q0 * 16 - 16);
-                }
-                fb[j] = join(x, y);
-            }
-            if (!kExact) {
+                const uint32_t byte = wb[j] & 255u;
 #pragma unroll
-                for (int i = 0; i < S::kFM; ++i)
+                for (int t = 0; t < 4; ++t)
+                    hb[j][t] = widen(poisoned(fb[kk][j][2 * t], byte), fb[kk][j][2 * t + 1], scale_value(byte));
+            }
+#pragma unroll
+            for (int i = 0; i < S::kFM; ++i) {
+                const uint32_t byte = wa[i] & 255u;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const bf16x8 ha = widen(poisoned(fa[kk][i][2 * t], byte), fa[kk][i][2 * t + 1], scale_value(byte));
 #pragma unroll
                     for (int j = 0; j < S::kFN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            fa[i], fb[j], acc[i][j], 0, 0, 0, static_cast<int>(wa[i] >> shift), 0,
-                            static_cast<int>(wb[j] >> shift));
-            } else {
-                bf16x8 hb[S::kFN][4];
-#pragma unroll
-                for (int j = 0; j < S::kFN; ++j) {
-                    const uint32_t byte = wb[j] >> shift & 255u;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        hb[j][t] = widen(poisoned(fb[j][2 * t], byte), fb[j][2 * t + 1], scale_value(byte));
-                }
-#pragma unroll
-                for (int i = 0; i < S::kFM; ++i) {
-                    const uint32_t byte = wa[i] >> shift & 255u;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const bf16x8 ha = widen(poisoned(fa[i][2 * t], byte), fa[i][2 * t + 1], scale_value(byte));
-#pragma unroll
-                        for (int j = 0; j < S::kFN; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ha, hb[j][t], acc[i][j], 0, 0, 0);
-                    }
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ha, hb[j][t], acc[i][j], 0, 0, 0);
                 }
             }
         }
     };
 
+    constexpr std::integral_constant<int, 0> k0{};
+    constexpr std::integral_constant<int, 1> k1{};
     if (first < last) {
-        load(first, 0);
-        __syncthreads();
-        for (int block = first; block < last; ++block) {
-            const int stage = (block - first) & 1;
-            if (block + 1 < last) load(block + 1, stage ^ 1);
-            if ((block & 3) == 0) {
-#pragma unroll
-                for (int i = 0; i < S::kFM; ++i) wa[i] = *reinterpret_cast<const uint32_t*>(sa[i] + block);
-#pragma unroll
-                for (int j = 0; j < S::kFN; ++j) wb[j] = *reinterpret_cast<const uint32_t*>(sb[j] + block);
-            }
-            if ((block + 1) * kB8 <= a.k)
-                multiply(block, stage, std::false_type());
-            else
-                multiply(block, stage, std::true_type());
-            __syncthreads();
+        const bool ragged = last == blocks && (a.k & (kB8 - 1)) != 0;
+        const int full = last - (ragged ? 1 : 0);
+        // Loads past the last block repeat it, into the place that nobody reads any more.
+        const auto load_ahead = [&](int block, auto slot) { load(block < last ? block : last - 1, slot); };
+        const auto step = [&](int block, auto slot) {
+            constexpr std::integral_constant<int, 1 - decltype(slot)::value> other{};
+            if ((block + 2 & 3) == 0 && block + 2 < last) load_scales(block + 2);
+            read(slot, k1);
+            multiply(k0);
+            interleave<S, kExact>();
+            arrive();
+            load_ahead(block + 2, slot);
+            read(other, k0);  // (past the last block: what is there, and not used)
+            multiply(k1);
+            read_scales(block + 1);
+            interleave<S, kExact>();
+        };
+        load_scales(first);
+        load(first, k0);
+        load_ahead(first + 1, k1);
+        arrive();
+        read(k0, k0);
+        read_scales(first);
+        int block = first;
+        for (; block + 1 < full; block += 2) {
+            step(block, k0);
+            step(block + 1, k1);
         }
+        if (block < full) step(block++, k0);
+        if (ragged) {
+            uint8_t* const at = full - first & 1 ? odd : even;
+            trim(block, at);
+            read_at(at, k0);
+            read_at(at, k1);
+            read_scales(block);
+            multiply(k0);
+            multiply(k1);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may outlive the workgroup's LDS
     }
 
     // A lane has kFN neighbouring columns of 16 rows of each of its squares.
@@ -466,7 +542,7 @@ void launch_few(const ProductArgs& a, hipStream_t s) {
         product_few_kernel<kType, kExact, 4><<<grid, kFewWaves * 64, 0, s>>>(a);
 }
 
-typedef Shape<256, 256, 2, 4> Large;
+typedef Shape<256, 256, 2, 2> Large;
 typedef Shape<128, 128, 2, 2> Small;
 
 template <int kType>
