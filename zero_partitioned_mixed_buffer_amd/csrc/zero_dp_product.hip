@@ -386,29 +386,55 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
     }
 
     // A lane has kFN neighbouring columns of 16 rows of each of its squares.
-    const int col = wn * 32 * S::kFN + r32 * S::kFN;
-    const int64_t left = a.b.rows - n0 - col;
-    if (left <= 0) return;
+    typedef typename Out<kType>::T T;
+    const int64_t corner = n0 + wn * 32 * S::kFN;
+    if (rows_a == S::kBM && rows_b == S::kBN && a.add == nullptr && parts == 1) {
+        // a whole tile: straight out of the registers
+        T* to = static_cast<T*>(a.out) + (m0 + wm * 32 * S::kFM + g * 4) * a.out_stride + corner + r32 * S::kFN;
 #pragma unroll
-    for (int i = 0; i < S::kFM; ++i)
+        for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float v[S::kFN];
+#pragma unroll
+                for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
+                store_run<T, S::kFN>(to, v, nullptr, S::kFN);
+                to += ((e & 3) == 3 ? 5 : 1) * a.out_stride;
+            }
+        return;
+    }
+    // Else 32 rows at a time through LDS, each wave in a place of its own, so
+    // that the masks and the addend come in a short loop.
+    constexpr int kWide = 32 * S::kFN;
+    static_assert(kWide * 32 * 4 * S::kWM * S::kWN <= S::kRows * kB8, "room for the waves' squares");
+    __syncthreads();  // the last block's reads
+    float* const mine = reinterpret_cast<float*>(even) + wave * kWide * 32;
+    const int64_t left = a.b.rows - corner - r32 * S::kFN;
+#pragma unroll
+    for (int i = 0; i < S::kFM; ++i) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const int p = wm * 32 * S::kFM + i * 32 + (e >> 2) * 8 + g * 4 + (e & 3);
-            if (p >= rows_a) continue;
-            float v[S::kFN];
+            typedef float V __attribute__((ext_vector_type(S::kFN)));
+            V v;
 #pragma unroll
             for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
-            const int64_t row = m0 + p;
-            if (parts > 1) {
-                float* to = a.part + (part * a.a.rows + row) * a.b.rows + n0 + col;
-                store_run<float, S::kFN>(to, v, nullptr, left);
-            } else {
-                typedef typename Out<kType>::T T;
-                T* to = static_cast<T*>(a.out) + row * a.out_stride + n0 + col;
-                const T* add = a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + n0 + col;
-                store_run<T, S::kFN>(to, v, add, left);
-            }
+            *reinterpret_cast<V*>(mine + ((e >> 2) * 8 + g * 4 + (e & 3)) * kWide + r32 * S::kFN) = v;
         }
+        const int p0 = wm * 32 * S::kFM + i * 32;
+        for (int r = g; r < 32; r += 2) {
+            if (p0 + r >= rows_a || left <= 0) break;
+            float v[S::kFN];
+#pragma unroll
+            for (int j = 0; j < S::kFN; ++j) v[j] = mine[r * kWide + r32 * S::kFN + j];
+            const int64_t row = m0 + p0 + r, col = corner + r32 * S::kFN;
+            if (parts > 1)
+                store_run<float, S::kFN>(a.part + (part * a.a.rows + row) * a.b.rows + col, v, nullptr, left);
+            else
+                store_run<T, S::kFN>(static_cast<T*>(a.out) + row * a.out_stride + col, v,
+                                     a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + col,
+                                     left);
+        }
+    }
 }
 
 // The parts' sum, in order, and the addend.
