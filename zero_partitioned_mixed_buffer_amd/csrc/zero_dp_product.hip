@@ -151,15 +151,18 @@ __device__ __forceinline__ rsrc_t buffer_of(const uint8_t* p) {
 
 __device__ __forceinline__ int place(int p, int q) { return p * kB8 + ((q ^ (p >> 1 & 7)) << 4); }
 
-// Asks the compiler to deal a half block's LDS reads out among its matrix
-// instructions, and to keep them on this side of what follows.
-template <typename S, bool kExact>
+// Asks the compiler to deal out a half block's LDS reads, two to a matrix
+// instruction until there are no more, and kLoads direct loads, one to each,
+// and to keep all of it on this side of what follows.
+template <typename S, bool kExact, int kLoads>
 __device__ __forceinline__ void interleave() {
     if (!kExact) {
+        constexpr int kN = S::kFM * S::kFN, kPer = (kLoads + kN - 1) / kN;
 #pragma unroll
-        for (int i = 0; i < S::kFM * S::kFN; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);    // a matrix instruction
-            __builtin_amdgcn_sched_group_barrier(0x100, (S::kReads + S::kFM * S::kFN - 1) / (S::kFM * S::kFN), 0);  // reads
+        for (int i = 0; i < kN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);  // a matrix instruction
+            if (i * 2 < S::kReads + (kLoads > 0 ? S::kFM + S::kFN : 0)) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            if (kLoads > 0) __builtin_amdgcn_sched_group_barrier(0x10, kPer, 0);
         }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -292,13 +295,21 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
         }
     };
     const auto read = [&](auto slot, auto half) { read_at(decltype(slot)::value ? odd : even, half); };
+    // The words with the scales of a block, and the words shifted to it.
+    uint32_t na[S::kFM], nb[S::kFN];
     const auto read_scales = [&](int block) {
         const uint32_t* const at = lds_scales[block >> 2 & 1];
+#pragma unroll
+        for (int i = 0; i < S::kFM; ++i) na[i] = at[wm * 32 * S::kFM + i * 32 + r32];
+#pragma unroll
+        for (int j = 0; j < S::kFN; ++j) nb[j] = at[S::kBM + wn * 32 * S::kFN + j * 32 + r32];
+    };
+    const auto take_scales = [&](int block) {
         const int shift = 8 * (block & 3);
 #pragma unroll
-        for (int i = 0; i < S::kFM; ++i) wa[i] = at[wm * 32 * S::kFM + i * 32 + r32] >> shift;
+        for (int i = 0; i < S::kFM; ++i) wa[i] = na[i] >> shift;
 #pragma unroll
-        for (int j = 0; j < S::kFN; ++j) wb[j] = at[S::kBM + wn * 32 * S::kFN + j * 32 + r32] >> shift;
+        for (int j = 0; j < S::kFN; ++j) wb[j] = nb[j] >> shift;
     };
 
     f32x16 acc[S::kFM][S::kFN];
@@ -353,13 +364,14 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
             if ((block + 2 & 3) == 0 && block + 2 < last) load_scales(block + 2);
             read(slot, k1);
             multiply(k0);
-            interleave<S, kExact>();
+            interleave<S, kExact, 0>();
             arrive();
             load_ahead(block + 2, slot);
             read(other, k0);  // (past the last block: what is there, and not used)
-            multiply(k1);
             read_scales(block + 1);
-            interleave<S, kExact>();
+            multiply(k1);
+            interleave<S, kExact, S::kLoadsA + S::kLoadsB>();
+            take_scales(block + 1);
         };
         load_scales(first);
         load(first, k0);
@@ -367,6 +379,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
         arrive();
         read(k0, k0);
         read_scales(first);
+        take_scales(first);
         int block = first;
         for (; block + 1 < full; block += 2) {
             step(block, k0);
@@ -378,7 +391,6 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
             trim(block, at);
             read_at(at, k0);
             read_at(at, k1);
-            read_scales(block);
             multiply(k0);
             multiply(k1);
         }
