@@ -82,10 +82,11 @@ __device__ __forceinline__ void store_run(T* to, const float (&v)[kN], const T* 
 }
 
 // ------------------------------------------------------------------- codes
-// 16 codes of which the first `left` count, the others zero.
-__device__ __forceinline__ i32x4 keep(i32x4 x, int left) {
+// Codes of which the first `left` count, the others zero.
+template <typename V>
+__device__ __forceinline__ V keep(V x, int left) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < static_cast<int>(sizeof(V) / 4); ++i) {
         const int b = left - 4 * i;
         x[i] = b >= 4 ? x[i] : b <= 0 ? 0 : x[i] & static_cast<int>((1u << (8 * b)) - 1u);
     }
@@ -263,18 +264,6 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(scales_b, (lds_ptr)(to + S::kBM + i * S::kThreads), 4,
                                                          static_cast<int>(off_sb[i]), block, 0, 0);
     };
-    // Makes the codes past the row's end zeros.
-    const auto trim = [&](int block, uint8_t* at) {
-        const int left = a.k - block * kB8;
-        for (int u = threadIdx.x; u < S::kRows * 8; u += S::kThreads) {
-            const int p = u >> 3, q = u & 7;
-            if (q * 16 + 16 <= left) continue;
-            i32x4* const x = reinterpret_cast<i32x4*>(at + place(p, q));
-            *x = keep(*x, left - q * 16);
-        }
-        arrive();
-    };
-
     const int r32 = lane & 31, g = lane >> 5;
     i32x8 fa[2][S::kFM], fb[2][S::kFN];
     uint32_t wa[S::kFM], wb[S::kFN];
@@ -295,6 +284,14 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
         }
     };
     const auto read = [&](auto slot, auto half) { read_at(decltype(slot)::value ? odd : even, half); };
+    // Of half a block in registers, `left` codes of a row count, the others become zeros.
+    const auto trim = [&](int left, auto half) {
+        constexpr int kk = decltype(half)::value;
+#pragma unroll
+        for (int i = 0; i < S::kFM; ++i) fa[kk][i] = keep(fa[kk][i], left - g * 32);
+#pragma unroll
+        for (int j = 0; j < S::kFN; ++j) fb[kk][j] = keep(fb[kk][j], left - g * 32);
+    };
     // The words with the scales of a block, and the words shifted to it.
     uint32_t na[S::kFM], nb[S::kFN];
     const auto read_scales = [&](int block) {
@@ -386,13 +383,15 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
             step(block + 1, k1);
         }
         if (block < full) step(block++, k0);
-        if (ragged) {
-            uint8_t* const at = full - first & 1 ? odd : even;
-            trim(block, at);
-            read_at(at, k0);
-            read_at(at, k1);
+        if (ragged) {  // its first half has been read
+            const int left = a.k - block * kB8;
+            if (left < kB8 / 2) trim(left, k0);
             multiply(k0);
-            multiply(k1);
+            if (left > kB8 / 2) {
+                read_at(full - first & 1 ? odd : even, k1);
+                trim(left - kB8 / 2, k1);
+                multiply(k1);
+            }
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may outlive the workgroup's LDS
     }
@@ -580,7 +579,7 @@ void launch_few(const ProductArgs& a, hipStream_t s) {
         product_few_kernel<kType, kExact, 4><<<grid, kFewWaves * 64, 0, s>>>(a);
 }
 
-typedef Shape<256, 256, 2, 2> Large;
+typedef Shape<256, 256, 2, 4> Large;
 typedef Shape<128, 128, 2, 2> Small;
 
 template <int kType>
