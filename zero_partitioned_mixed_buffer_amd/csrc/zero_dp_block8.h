@@ -33,20 +33,41 @@ constexpr int64_t kProductMaxTiles = 1 << 22;
 
 inline int64_t product_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256); }
 
-// Which of the product's kernels takes a size.
-enum ProductShape { kProductFew, kProductSmall, kProductLarge };
+// Which of the product's kernels takes a size: few rows, or tiles of 128 x 128
+// (two workgroups to a CU), 192 x 256 or 256 x 256 (one).
+enum ProductShape { kProductFew, kProductSmall, kProductMedium, kProductLarge };
 
-inline ProductShape product_shape(int64_t m, int64_t n) {
-    if (m <= 64) return kProductFew;
-    return product_tiles(m, n) >= 128 ? kProductLarge : kProductSmall;
+constexpr int64_t kProductCus = 256;  // of an MI355X; the choice costs time alone
+
+// Tiles of 256 x 256 past the last full round that are taken in quarters: up
+// to one quarter to a CU.
+inline int64_t product_rest(int64_t tiles) {
+    const int64_t rest = tiles % kProductCus;
+    return tiles > kProductCus && rest <= kProductCus / 4 ? rest : 0;
 }
 
-// Parts that a product's sum over k is split into (more than one: each part's
-// fp32 sums go to the workspace, and a second launch adds them up).
+// By the time that the slowest CU takes, in hundredths of a 256 x 256 tile's.
+inline ProductShape product_shape(int64_t m, int64_t n, bool exact) {
+    if (m <= 64) return kProductFew;
+    const int64_t small = ((m + 127) / 128) * ((n + 127) / 128);
+    if (small <= kProductCus) return kProductSmall;
+    const int64_t medium = ((m + 191) / 192) * ((n + 255) / 256), large = product_tiles(m, n);
+    const auto rounds = [](int64_t tiles) { return (tiles + kProductCus - 1) / kProductCus; };
+    const int64_t cost_small = (rounds(small) + 1) / 2 * (exact ? 55 : 70);
+    const int64_t cost_medium = rounds(medium) * 78;
+    const int64_t cost_large =
+        product_rest(large) > 0 ? large / kProductCus * 100 + (exact ? 35 : 50) : rounds(large) * 100;
+    if (cost_large <= cost_medium && cost_large <= cost_small) return kProductLarge;
+    return cost_medium <= cost_small ? kProductMedium : kProductSmall;
+}
+
+// Parts that a product's sum over k is split into where there are few tiles
+// (more than one: each part's fp32 sums go to the workspace, and a second
+// launch adds them up).
 inline int product_parts(int64_t m, int64_t n, int64_t k) {
-    if (product_shape(m, n) != kProductSmall) return 1;
     const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
-    int64_t parts = 512 / tiles;
+    if (m <= 64 || tiles > kProductCus) return 1;
+    int64_t parts = 2 * kProductCus / tiles;
     const int64_t most = k / 1024;
     parts = parts < most ? parts : most;
     if (parts < 2) return 1;

@@ -111,6 +111,11 @@ __device__ __forceinline__ const uint8_t* scale_row(const ProductSide& s, int64_
     return s.scales + (row >> s.shift) * s.scales_stride;
 }
 
+// From the scales of row r0 to those of row r0 + p.
+__device__ __forceinline__ uint32_t scale_offset(const ProductSide& s, int64_t r0, int p) {
+    return static_cast<uint32_t>(((r0 + p) >> s.shift) - (r0 >> s.shift)) * static_cast<uint32_t>(s.scales_stride);
+}
+
 // ------------------------------------------------------------------- tiles
 // A workgroup computes kBM x kBN of out with kWM x kWN waves, each of them
 // kFM x kFN squares of 32.  Blocks of 128 k of both operands go to one of two
@@ -176,31 +181,18 @@ __device__ __forceinline__ void arrive() {
     asm volatile("" ::: "memory");
 }
 
+// The tile whose first element is (m0, n0), over part `part` of k.  even and
+// odd are two objects, so that the compiler sees that loads into one do not
+// touch reads of the other.
 template <typename S, int kType, bool kExact>
-__global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int parts) {
-    // two objects, so that the compiler sees that loads into one do not touch reads of the other
-    __shared__ __attribute__((aligned(1024))) uint8_t even[S::kRows * kB8];
-    __shared__ __attribute__((aligned(1024))) uint8_t odd[S::kRows * kB8];
-    __shared__ uint32_t lds_scales[2][S::kRows];
+__device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, int64_t m0, int64_t n0, uint8_t* even,
+                                     uint8_t* odd, uint32_t* lds_scales) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::kWN, wn = wave % S::kWN;
 
-    // Consecutive workgroups go to the eight dies in turn; each die takes a
-    // run of neighbouring tiles, whose operands then meet in its L2 ...
-    const uint32_t tm = static_cast<uint32_t>((a.a.rows + S::kBM - 1) / S::kBM);
-    const uint32_t tn = static_cast<uint32_t>((a.b.rows + S::kBN - 1) / S::kBN);
-    const uint32_t tiles = tm * tn, die = blockIdx.x & 7, rest = tiles & 7;
-    const uint32_t id = die * (tiles >> 3) + (die < rest ? die : rest) + (blockIdx.x >> 3);
-    // ... in bands of 8 tile rows, column by column
-    const uint32_t band = id / (8 * tn), in_band = id - band * 8 * tn;
-    const uint32_t high = tm - band * 8 < 8 ? tm - band * 8 : 8;
-    const uint32_t across = in_band / high;
-    const int64_t m0 = static_cast<int64_t>(band * 8 + in_band - across * high) * S::kBM;
-    const int64_t n0 = static_cast<int64_t>(across) * S::kBN;
-
     const int blocks = (a.k + kB8 - 1) / kB8;
     // parts begin at a multiple of four blocks (a word of scales)
-    const int part = blockIdx.y, per = ((blocks + parts - 1) / parts + 3) & ~3;
+    const int per = ((blocks + parts - 1) / parts + 3) & ~3;
     const int first = part * per, last = first + per < blocks ? first + per : blocks;
 
     // Rows past the end repeat the last one (their results are not stored).
@@ -245,14 +237,12 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
     uint32_t off_sa[S::kScalesA], off_sb[S::kScalesB];
 #pragma unroll
     for (int i = 0; i < S::kScalesA; ++i)
-        off_sa[i] = static_cast<uint32_t>(row_of_a(i * S::kThreads + static_cast<int>(threadIdx.x)) >> a.a.shift) *
-                    static_cast<uint32_t>(a.a.scales_stride);
+        off_sa[i] = scale_offset(a.a, m0, row_of_a(i * S::kThreads + static_cast<int>(threadIdx.x)));
 #pragma unroll
     for (int i = 0; i < S::kScalesB; ++i)
-        off_sb[i] = static_cast<uint32_t>(row_of_b(i * S::kThreads + static_cast<int>(threadIdx.x)) >> a.b.shift) *
-                    static_cast<uint32_t>(a.b.scales_stride);
+        off_sb[i] = scale_offset(a.b, n0, row_of_b(i * S::kThreads + static_cast<int>(threadIdx.x)));
     const auto load_scales = [&](int block) {
-        uint32_t* const to = lds_scales[block >> 2 & 1] + wave * 64;
+        uint32_t* const to = lds_scales + (block >> 2 & 1) * S::kRows + wave * 64;
 #pragma unroll
         for (int i = 0; i < S::kScalesA; ++i)
             if ((i + 1) * S::kThreads <= S::kBM || i * S::kThreads + wave * 64 < S::kBM)
@@ -267,21 +257,18 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
     const int r32 = lane & 31, g = lane >> 5;
     i32x8 fa[2][S::kFM], fb[2][S::kFN];
     uint32_t wa[S::kFM], wb[S::kFN];
+    // Piece 2 g of the lane's rows; the other pieces and the other rows of a wave lie at fixed distances.
+    const int at_a = place(wm * 32 * S::kFM + r32, g * 2), at_b = place(S::kBM + wn * 32 * S::kFN + r32, g * 2);
     const auto read_at = [&](const uint8_t* at, auto half) {
         constexpr int kk = decltype(half)::value;
-        const int q = kk * 4 + g * 2;
 #pragma unroll
-        for (int i = 0; i < S::kFM; ++i) {
-            const int p = wm * 32 * S::kFM + i * 32 + r32;
-            fa[kk][i] = join(*reinterpret_cast<const i32x4*>(at + place(p, q)),
-                             *reinterpret_cast<const i32x4*>(at + place(p, q + 1)));
-        }
+        for (int i = 0; i < S::kFM; ++i)
+            fa[kk][i] = join(*reinterpret_cast<const i32x4*>(at + (at_a ^ kk * 64) + i * 32 * kB8),
+                             *reinterpret_cast<const i32x4*>(at + (at_a ^ (kk * 64 + 16)) + i * 32 * kB8));
 #pragma unroll
-        for (int j = 0; j < S::kFN; ++j) {
-            const int p = S::kBM + wn * 32 * S::kFN + j * 32 + r32;
-            fb[kk][j] = join(*reinterpret_cast<const i32x4*>(at + place(p, q)),
-                             *reinterpret_cast<const i32x4*>(at + place(p, q + 1)));
-        }
+        for (int j = 0; j < S::kFN; ++j)
+            fb[kk][j] = join(*reinterpret_cast<const i32x4*>(at + (at_b ^ kk * 64) + j * 32 * kB8),
+                             *reinterpret_cast<const i32x4*>(at + (at_b ^ (kk * 64 + 16)) + j * 32 * kB8));
     };
     const auto read = [&](auto slot, auto half) { read_at(decltype(slot)::value ? odd : even, half); };
     // Of half a block in registers, `left` codes of a row count, the others become zeros.
@@ -295,7 +282,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
     // The words with the scales of a block, and the words shifted to it.
     uint32_t na[S::kFM], nb[S::kFN];
     const auto read_scales = [&](int block) {
-        const uint32_t* const at = lds_scales[block >> 2 & 1];
+        const uint32_t* const at = lds_scales + (block >> 2 & 1) * S::kRows;
 #pragma unroll
         for (int i = 0; i < S::kFM; ++i) na[i] = at[wm * 32 * S::kFM + i * 32 + r32];
 #pragma unroll
@@ -417,9 +404,10 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
     // Else 32 rows at a time through LDS, each wave in a place of its own, so
     // that the masks and the addend come in a short loop.
     constexpr int kWide = 32 * S::kFN;
-    static_assert(kWide * 32 * 4 * S::kWM * S::kWN <= S::kRows * kB8, "room for the waves' squares");
+    constexpr int kHalf = S::kWM * S::kWN / 2;
+    static_assert(kWide * 32 * 4 * kHalf <= S::kRows * kB8, "room for the waves' squares");
     __syncthreads();  // the last block's reads
-    float* const mine = reinterpret_cast<float*>(even) + wave * kWide * 32;
+    float* const mine = reinterpret_cast<float*>(wave < kHalf ? even : odd) + wave % kHalf * kWide * 32;
     const int64_t left = a.b.rows - corner - r32 * S::kFN;
 #pragma unroll
     for (int i = 0; i < S::kFM; ++i) {
@@ -446,6 +434,45 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int
                                      left);
         }
     }
+}
+
+// Tile `id` of tiles of `high` x `wide`: in bands of 8 tile rows, column by column.
+__device__ __forceinline__ void corner_of(uint32_t id, const ProductArgs& a, int high, int wide, int64_t& m0,
+                                          int64_t& n0) {
+    const uint32_t tm = static_cast<uint32_t>((a.a.rows + high - 1) / high);
+    const uint32_t tn = static_cast<uint32_t>((a.b.rows + wide - 1) / wide);
+    const uint32_t band = id / (8 * tn), in_band = id - band * 8 * tn;
+    const uint32_t rows = tm - band * 8 < 8 ? tm - band * 8 : 8, across = in_band / rows;
+    m0 = static_cast<int64_t>(band * 8 + in_band - across * rows) * high;
+    n0 = static_cast<int64_t>(across) * wide;
+}
+
+// The first `count` tiles of shape S.  Consecutive workgroups go to the eight
+// dies in turn; each die takes a run of neighbouring tiles, whose operands
+// then meet in its L2.
+template <typename S, int kType>
+__global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int parts, uint32_t count) {
+    __shared__ __attribute__((aligned(1024))) uint8_t even[S::kRows * kB8];
+    __shared__ __attribute__((aligned(1024))) uint8_t odd[S::kRows * kB8];
+    __shared__ uint32_t lds_scales[2 * S::kRows];
+    const uint32_t die = blockIdx.x & 7, more = count & 7;
+    int64_t m0, n0;
+    corner_of(die * (count >> 3) + (die < more ? die : more) + (blockIdx.x >> 3), a, S::kBM, S::kBN, m0, n0);
+    tile<S, kType, kType == ZERO_TYPE_F32>(a, parts, blockIdx.y, m0, n0, even, odd, lds_scales);
+}
+
+// The tiles from `first` on of twice S's size, each as four of shape S.
+template <typename S, int kType>
+__global__ __launch_bounds__(S::kThreads) void product_rest_kernel(ProductArgs a, uint32_t first) {
+    __shared__ __attribute__((aligned(1024))) uint8_t even[S::kRows * kB8];
+    __shared__ __attribute__((aligned(1024))) uint8_t odd[S::kRows * kB8];
+    __shared__ uint32_t lds_scales[2 * S::kRows];
+    int64_t m0, n0;
+    corner_of(first + (blockIdx.x >> 2), a, 2 * S::kBM, 2 * S::kBN, m0, n0);
+    m0 += (blockIdx.x >> 1 & 1) * S::kBM;
+    n0 += (blockIdx.x & 1) * S::kBN;
+    if (m0 < a.a.rows && n0 < a.b.rows)
+        tile<S, kType, kType == ZERO_TYPE_F32>(a, 1, 0, m0, n0, even, odd, lds_scales);
 }
 
 // The parts' sum, in order, and the addend.
@@ -555,18 +582,6 @@ int finish() {
     return ZERO_EHIP;
 }
 
-template <typename S, int kType>
-void launch_tiles(const ProductArgs& a, int parts, hipStream_t s) {
-    constexpr bool kExact = kType == ZERO_TYPE_F32;
-    const int64_t tiles = ((a.a.rows + S::kBM - 1) / S::kBM) * ((a.b.rows + S::kBN - 1) / S::kBN);
-    product_kernel<S, kType, kExact>
-        <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(parts)), S::kThreads, 0, s>>>(a, parts);
-    if (parts > 1) {
-        const int64_t units = (a.a.rows * ((a.b.rows + 3) / 4) + 255) / 256;
-        join_parts_kernel<kType><<<static_cast<unsigned>(units < 8192 ? units : 8192), 256, 0, s>>>(a, parts);
-    }
-}
-
 template <int kType>
 void launch_few(const ProductArgs& a, hipStream_t s) {
     constexpr bool kExact = kType == ZERO_TYPE_F32;
@@ -580,13 +595,30 @@ void launch_few(const ProductArgs& a, hipStream_t s) {
 }
 
 typedef Shape<256, 256, 2, 4> Large;
+typedef Shape<192, 256, 2, 4> Medium;
 typedef Shape<128, 128, 2, 2> Small;
+static_assert(Large::kBM == 2 * Small::kBM && Large::kBN == 2 * Small::kBN, "a large tile is four small ones");
+
+template <typename S, int kType>
+void launch_tiles(const ProductArgs& a, int parts, hipStream_t s) {
+    const int64_t tiles = ((a.a.rows + S::kBM - 1) / S::kBM) * ((a.b.rows + S::kBN - 1) / S::kBN);
+    const int64_t rest = std::is_same<S, Large>::value ? zdp::product_rest(tiles) : 0;
+    const uint32_t count = static_cast<uint32_t>(tiles - rest);
+    product_kernel<S, kType><<<dim3(count, static_cast<unsigned>(parts)), S::kThreads, 0, s>>>(a, parts, count);
+    if (rest > 0)
+        product_rest_kernel<Small, kType><<<static_cast<unsigned>(4 * rest), Small::kThreads, 0, s>>>(a, count);
+    if (parts > 1) {
+        const int64_t units = (a.a.rows * ((a.b.rows + 3) / 4) + 255) / 256;
+        join_parts_kernel<kType><<<static_cast<unsigned>(units < 8192 ? units : 8192), 256, 0, s>>>(a, parts);
+    }
+}
 
 template <int kType>
 void launch_typed(const ProductArgs& a, int parts, hipStream_t s) {
-    switch (zdp::product_shape(a.a.rows, a.b.rows)) {
+    switch (zdp::product_shape(a.a.rows, a.b.rows, kType == ZERO_TYPE_F32)) {
         case zdp::kProductFew: launch_few<kType>(a, s); break;
         case zdp::kProductSmall: launch_tiles<Small, kType>(a, parts, s); break;
+        case zdp::kProductMedium: launch_tiles<Medium, kType>(a, parts, s); break;
         default: launch_tiles<Large, kType>(a, parts, s); break;
     }
 }
