@@ -174,28 +174,59 @@ __device__ __forceinline__ void load_vector(const void* w, int type, int c, int 
 }
 
 // ------------------------------------------------------------- reductions
-// Largest value over the 16 lanes of a DPP row.
-__device__ __forceinline__ uint32_t max16(uint32_t x) {
-    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xF, 0xF, true)));   // lane ^ 1
-    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xF, 0xF, true)));   // lane ^ 2
-    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x141, 0xF, 0xF, true)));  // other half of 8
-    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x140, 0xF, 0xF, true)));  // other half of 16
-    return x;
+// A register's value in another lane of the same DPP row of 16: lane ^ 1, lane
+// ^ 2, the mirrored lane of the 8 and of the 16.
+template <int kStep>
+__device__ __forceinline__ uint32_t swap16(uint32_t x) {
+    constexpr int kCtl = kStep == 0 ? 0xB1 : kStep == 1 ? 0x4E : kStep == 2 ? 0x141 : 0x140;
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kCtl, 0xF, 0xF, true));
+}
+template <int kStep>
+__device__ __forceinline__ float swap16(float x) {
+    return float_of(swap16<kStep>(bits_of(x)));
+}
+template <int kStep>
+__device__ __forceinline__ double swap16(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint64_t lo = swap16<kStep>(static_cast<uint32_t>(b)), hi = swap16<kStep>(static_cast<uint32_t>(b >> 32));
+    return __builtin_bit_cast(double, hi << 32 | lo);
 }
 
-// Sum over a row's waves, the same in every lane.
+__device__ __forceinline__ uint32_t lane_of(uint32_t x, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
+}
+__device__ __forceinline__ float lane_of(float x, int lane) { return float_of(lane_of(bits_of(x), lane)); }
+__device__ __forceinline__ double lane_of(double x, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint64_t lo = lane_of(static_cast<uint32_t>(b), lane), hi = lane_of(static_cast<uint32_t>(b >> 32), lane);
+    return __builtin_bit_cast(double, hi << 32 | lo);
+}
+
+// Largest value over the 16 lanes of a DPP row.
+__device__ __forceinline__ uint32_t max16(uint32_t x) {
+    x = max(x, swap16<0>(x));
+    x = max(x, swap16<1>(x));
+    x = max(x, swap16<2>(x));
+    return max(x, swap16<3>(x));
+}
+
+// Sum over a row's waves, the same in every lane.  `turn` counts the
+// workgroup's sums: two places in LDS, used in turn, need one barrier a sum.
 template <int kWaves, typename F>
-__device__ __forceinline__ F row_sum(F x) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+__device__ __forceinline__ F row_sum(F x, int turn) {
+    x += swap16<0>(x);
+    x += swap16<1>(x);
+    x += swap16<2>(x);
+    x += swap16<3>(x);
+    x = (lane_of(x, 0) + lane_of(x, 16)) + (lane_of(x, 32) + lane_of(x, 48));
     if (kWaves > 1) {
-        __shared__ F s[kWaves];
-        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+        __shared__ F s[2][kWaves];
+        F* const at = s[turn & 1];
+        if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = x;
         __syncthreads();
-        x = s[0];
+        x = at[0];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) x += s[w];
-        __syncthreads();
+        for (int w = 1; w < kWaves; ++w) x += at[w];
     }
     return x;
 }
@@ -242,10 +273,9 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, uint32_t
 // single bytes at the end of the row.
 __device__ __forceinline__ void store_scales(uint8_t* row, int c0, int n, uint32_t byte) {
     const int lane = threadIdx.x & 63, b0 = c0 / kB8, nb = (n + kB8 - 1) / kB8;
-    uint32_t word = byte << (8 * (lane >> 4));
-    word |= __shfl_xor(word, 16);
-    word |= __shfl_xor(word, 32);
     if (b0 + 4 <= nb) {
+        const uint32_t word =
+            lane_of(byte, 0) | lane_of(byte, 16) << 8 | lane_of(byte, 32) << 16 | lane_of(byte, 48) << 24;
         if (lane == 0) *reinterpret_cast<uint32_t*>(row + b0) = word;
     } else if ((lane & 15) == 0 && b0 + (lane >> 4) < nb) {
         row[b0 + (lane >> 4)] = static_cast<uint8_t>(byte);
@@ -298,50 +328,68 @@ __device__ __forceinline__ void scaled(const float (&h)[kU], float rstd, const f
 
 // ------------------------------------------------------------------- norm
 // kWaves waves hold a row in registers, kNS units a lane.  Rows of one wave
-// need no barrier; four of them make a workgroup.
+// need no barrier; kPack of them make a workgroup.  A workgroup takes rows in
+// turn, the next one's loads under way while this one is worked on, and keeps
+// its columns' weights in registers.
 template <int kWaves>
-constexpr int kThreads = kWaves == 1 ? 256 : 64 * kWaves;
+constexpr int kPack = kWaves == 1 ? 4 : 1;
 template <int kWaves>
-constexpr int kGroupRows = kWaves == 1 ? 4 : 1;
+constexpr int kThreads = 64 * kWaves * kPack<kWaves>;
+
+// A vector's units of a lane.
+template <int kWaves, int kNS>
+__device__ __forceinline__ void load_weights(const void* w, int type, int c0, int n, float (&v)[kNS][kU]) {
+#pragma unroll
+    for (int s = 0; s < kNS; ++s) load_vector(w, type, c0 + s * kWaves * kSweep, n, v[s]);
+}
+
+// A row's units of a lane.
+template <int kType, int kWaves, int kNS>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t stride, int c0, int n,
+                                         Raw<kType> (&x)[kNS]) {
+    const char* from = row_of<kType>(p, row, stride);
+#pragma unroll
+    for (int s = 0; s < kNS; ++s) x[s] = load_unit<kType>(from, c0 + s * kWaves * kSweep, n);
+}
 
 template <int kType, bool kRes, int kWaves, int kNS>
 __global__ __launch_bounds__(kThreads<kWaves>) void norm8_kernel(NormArgs a) {
     const int c0 = (kWaves == 1 ? threadIdx.x & 63 : threadIdx.x) * kU;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroupRows<kWaves>;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kGroupRows<kWaves> + (kWaves == 1 ? threadIdx.x >> 6 : 0);
-         row < a.rows; row += step) {
-        const char* x = row_of<kType>(a.x, row, a.x_stride);
-        const char* r = row_of<kType>(a.r, row, a.r_stride);
-        char* h = row_of<kType>(a.h, row, a.h_stride);
-        Raw<kType> rx[kNS], rr[kNS];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kPack<kWaves>;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kPack<kWaves> + (kWaves == 1 ? threadIdx.x >> 6 : 0);
+    if (row >= a.rows) return;
+    Raw<kType> nx[kNS], nr[kNS];
+    load_row<kType, kWaves>(a.x, row, a.x_stride, c0, a.cols, nx);
+    if (kRes) load_row<kType, kWaves>(a.r, row, a.r_stride, c0, a.cols, nr);
+    float w[kNS][kU];
+    load_weights<kWaves>(a.w, a.w_type, c0, a.cols, w);
+    for (int turn = 0; row < a.rows; row += step, ++turn) {
         float v[kNS][kU];
-#pragma unroll
-        for (int s = 0; s < kNS; ++s) rx[s] = load_unit<kType>(x, c0 + s * kWaves * kSweep, a.cols);
-        if (kRes) {
-#pragma unroll
-            for (int s = 0; s < kNS; ++s) rr[s] = load_unit<kType>(r, c0 + s * kWaves * kSweep, a.cols);
-        }
         double sum = 0.0;
+        char* h = row_of<kType>(a.h, row, a.h_stride);
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
             const int c = c0 + s * kWaves * kSweep;
             if (kRes) {
-                const Raw<kType> y = add_units(rx[s], rr[s], v[s]);
+                const Raw<kType> y = add_units(nx[s], nr[s], v[s]);
                 if (c < a.cols) store_unit(h, c, a.cols, y);
             } else {
-                unpack(rx[s], v[s]);
+                unpack(nx[s], v[s]);
             }
             sum = square_sum(v[s], sum);
         }
-        const float rstd = rstd_of(row_sum<kWaves>(sum), a.cols, a.eps);
+        if (row + step < a.rows) {
+            load_row<kType, kWaves>(a.x, row + step, a.x_stride, c0, a.cols, nx);
+            if (kRes) load_row<kType, kWaves>(a.r, row + step, a.r_stride, c0, a.cols, nr);
+        }
+        const float rstd = rstd_of(row_sum<kWaves>(sum, turn), a.cols, a.eps);
         if (c0 == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
             const int c = c0 + s * kWaves * kSweep;
             if ((c & ~(kSweep - 1)) >= a.cols) break;  // the whole wave
-            float w[kU], y[kU];
-            load_vector(a.w, a.w_type, c, a.cols, w);
-            scaled(v[s], rstd, w, y);
+            float y[kU];
+            scaled(v[s], rstd, w[s], y);
             emit(a.codes + row * a.codes_stride, a.scales + row * a.scales_stride, c, a.cols, y);
         }
     }
@@ -355,7 +403,8 @@ template <int kType, bool kRes>
 __global__ __launch_bounds__(kLongWaves * 64) void norm8_long_kernel(NormArgs a) {
     constexpr int kStep = kLongWaves * kSweep;
     const int c0 = threadIdx.x * kU;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
         const char* x = row_of<kType>(a.x, row, a.x_stride);
         const char* r = row_of<kType>(a.r, row, a.r_stride);
         char* h = row_of<kType>(a.h, row, a.h_stride);
@@ -369,7 +418,7 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm8_long_kernel(NormArgs a)
                 unpack(rx, v);
             sum = square_sum(v, sum);
         }
-        const float rstd = rstd_of(row_sum<kLongWaves>(sum), a.cols, a.eps);
+        const float rstd = rstd_of(row_sum<kLongWaves>(sum, turn), a.cols, a.eps);
         if (threadIdx.x == 0) a.rstd[row] = rstd;
         for (int c = c0; (c & ~(kSweep - 1)) < a.cols; c += kStep) {
             float v[kU], w[kU], y[kU];
@@ -406,50 +455,53 @@ __device__ __forceinline__ Raw<kType> grad_unit(const float (&g)[kU], const floa
     return pack<kType>(v);
 }
 
-// Each workgroup takes rows in turn and keeps its part of dweight in
+// As the norm's kernel; each workgroup keeps its part of dweight in
 // registers, one row of `part` at the end.
 template <int kType, int kWaves, int kNS>
 __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBackArgs a) {
     const int c0 = (kWaves == 1 ? threadIdx.x & 63 : threadIdx.x) * kU;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroupRows<kWaves>;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kPack<kWaves>;
     const bool has_dh = a.dh != nullptr;
-    float dw[kNS][kU];
+    float dw[kNS][kU], w[kNS][kU];
 #pragma unroll
     for (int s = 0; s < kNS; ++s)
 #pragma unroll
         for (int i = 0; i < kU; ++i) dw[s][i] = 0.0f;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kGroupRows<kWaves> + (kWaves == 1 ? threadIdx.x >> 6 : 0);
-         row < a.rows; row += step) {
-        const float rstd = a.rstd[row];
-        Raw<kType> ry[kNS], rh[kNS], rd[kNS];
-#pragma unroll
-        for (int s = 0; s < kNS; ++s) {
-            const int c = c0 + s * kWaves * kSweep;
-            ry[s] = load_unit<kType>(row_of<kType>(a.dy, row, a.dy_stride), c, a.cols);
-            rh[s] = load_unit<kType>(row_of<kType>(a.h, row, a.h_stride), c, a.cols);
-            if (has_dh) rd[s] = load_unit<kType>(row_of<kType>(a.dh, row, a.dh_stride), c, a.cols);
-        }
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kPack<kWaves> + (kWaves == 1 ? threadIdx.x >> 6 : 0);
+    Raw<kType> ny[kNS], nh[kNS], nd[kNS];
+    float nrstd = 0.0f;
+    const auto load = [&](int64_t at) {
+        if (at >= a.rows) return;
+        load_row<kType, kWaves>(a.dy, at, a.dy_stride, c0, a.cols, ny);
+        load_row<kType, kWaves>(a.h, at, a.h_stride, c0, a.cols, nh);
+        nrstd = a.rstd[at];
+    };
+    load(row);
+    load_weights<kWaves>(a.w, a.w_type, c0, a.cols, w);
+    for (int turn = 0; row < a.rows; row += step, ++turn) {
+        const float rstd = nrstd;
+        if (has_dh) load_row<kType, kWaves>(a.dh, row, a.dh_stride, c0, a.cols, nd);
         float g[kNS][kU], xh[kNS][kU], sum = 0.0f;
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
-            float dy[kU], h[kU], w[kU];
-            load_vector(a.w, a.w_type, c0 + s * kWaves * kSweep, a.cols, w);
-            unpack(ry[s], dy);
-            unpack(rh[s], h);
-            parts_of(dy, h, w, rstd, g[s], xh[s]);
+            float dy[kU], h[kU];
+            unpack(ny[s], dy);
+            unpack(nh[s], h);
+            parts_of(dy, h, w[s], rstd, g[s], xh[s]);
 #pragma unroll
             for (int i = 0; i < kU; ++i) {
                 sum += g[s][i] * xh[s][i];
                 dw[s][i] += dy[i] * xh[s][i];
             }
         }
-        const float c = row_sum<kWaves>(sum) / static_cast<float>(a.cols);
+        load(row + step);
+        const float c = row_sum<kWaves>(sum, turn) / static_cast<float>(a.cols);
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
             const int at = c0 + s * kWaves * kSweep;
             if (at < a.cols)
                 store_unit(row_of<kType>(a.dx, row, a.dx_stride), at, a.cols,
-                           grad_unit<kType>(g[s], xh[s], c, rstd, has_dh, rd[s]));
+                           grad_unit<kType>(g[s], xh[s], c, rstd, has_dh, nd[s]));
         }
     }
     if (a.dw == nullptr) return;
@@ -461,7 +513,8 @@ __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBa
 #pragma unroll
             for (int i = 0; i < kU; ++i) all[threadIdx.x >> 6][s * kSweep + c0 + i] = dw[s][i];
         __syncthreads();
-        for (int c = threadIdx.x; c < a.cols; c += 256) part[c] = (all[0][c] + all[1][c]) + (all[2][c] + all[3][c]);
+        for (int c = threadIdx.x; c < a.cols; c += kThreads<kWaves>)
+            part[c] = (all[0][c] + all[1][c]) + (all[2][c] + all[3][c]);
         return;
     }
 #pragma unroll
@@ -481,8 +534,8 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm8_backward_long_kernel(No
     const int c0 = threadIdx.x * kU;
     const bool has_dh = a.dh != nullptr;
     float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
-    bool first = true;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, first = false) {
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
         const float rstd = a.rstd[row];
         const char* dy_row = row_of<kType>(a.dy, row, a.dy_stride);
         const char* h_row = row_of<kType>(a.h, row, a.h_stride);
@@ -496,10 +549,10 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm8_backward_long_kernel(No
 #pragma unroll
             for (int i = 0; i < kU; ++i) {
                 sum += g[i] * xh[i];
-                if (a.dw != nullptr && c + i < a.cols) part[c + i] = (first ? 0.0f : part[c + i]) + dy[i] * xh[i];
+                if (a.dw != nullptr && c + i < a.cols) part[c + i] = (turn == 0 ? 0.0f : part[c + i]) + dy[i] * xh[i];
             }
         }
-        const float mean = row_sum<kLongWaves>(sum) / static_cast<float>(a.cols);
+        const float mean = row_sum<kLongWaves>(sum, turn) / static_cast<float>(a.cols);
         for (int c = c0; c < a.cols; c += kStep) {
             float dy[kU], h[kU], w[kU], g[kU], xh[kU];
             Raw<kType> rd = {};
@@ -715,12 +768,24 @@ void with_row_shape(int n, F f) {
     else if (n <= 8 * kSweep)
         f(integral_constant<int, 4>(), integral_constant<int, 2>());
     else if (n <= 16 * kSweep)
-        f(integral_constant<int, 4>(), integral_constant<int, 4>());
+        f(integral_constant<int, 8>(), integral_constant<int, 2>());
     else if (n <= 32 * kSweep)
-        f(integral_constant<int, 16>(), integral_constant<int, 2>());
+        f(integral_constant<int, 8>(), integral_constant<int, 4>());
     else
         f(integral_constant<int, 0>(), integral_constant<int, 0>());
 }
+
+// Workgroups of the norm's kernels: enough rows under way to cover memory's
+// latency, few enough that each goes on to a next row.
+constexpr int kNormWavesPerCu = 16;
+template <int kWaves>
+constexpr int64_t kNormGroups = 256 * kNormWavesPerCu / (kWaves * kPack<kWaves>);
+
+constexpr int kBackWavesPerCu = 8;
+template <int kWaves>
+constexpr int64_t kBackGroups = 256 * kBackWavesPerCu / (kWaves * kPack<kWaves>) < 256
+                                    ? 256
+                                    : 256 * kBackWavesPerCu / (kWaves * kPack<kWaves>);
 
 }  // namespace
 
@@ -739,7 +804,8 @@ int launch_norm8(const NormArgs& a, void* stream) {
                 else
                     norm8_long_kernel<kType, false><<<grid, kLongWaves * 64, 0, s>>>(a);
             } else {
-                const unsigned grid = grid_of((a.rows - 1) / kGroupRows<kWaves> + 1);
+                const int64_t most = (a.rows - 1) / kPack<kWaves> + 1;
+                const unsigned grid = static_cast<unsigned>(most < kNormGroups<kWaves> ? most : kNormGroups<kWaves>);
                 if (a.r != nullptr)
                     norm8_kernel<kType, true, kWaves, kNS><<<grid, kThreads<kWaves>, 0, s>>>(a);
                 else
@@ -761,8 +827,9 @@ int launch_norm8_backward(const NormBackArgs& a, void* stream) {
                 if constexpr (kWaves == 0) {
                     norm8_backward_long_kernel<kType><<<static_cast<unsigned>(groups), kLongWaves * 64, 0, s>>>(a);
                 } else {
-                    const int64_t most = (a.rows - 1) / kGroupRows<kWaves> + 1;
+                    const int64_t most = (a.rows - 1) / kPack<kWaves> + 1;
                     groups = groups < most ? groups : most;
+                    groups = groups < kBackGroups<kWaves> ? groups : kBackGroups<kWaves>;
                     norm8_backward_kernel<kType, kWaves, kNS>
                         <<<static_cast<unsigned>(groups), kThreads<kWaves>, 0, s>>>(a);
                 }
