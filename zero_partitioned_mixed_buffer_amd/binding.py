@@ -513,9 +513,15 @@ def _check_operand(t, n: int, kinds: Tuple[str, ...], what: str, cur: int):
         _check_current(t, what, cur)
 
 
+_get_device = None
+
+
 def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    global _get_device
+    if _get_device is None:
+        import torch
+        _get_device = torch.cuda.current_device
+    return _get_device()
 
 
 def _column(tensors: Sequence, numels: Sequence[int], kinds: Tuple[str, ...], what: str,
@@ -719,47 +725,70 @@ def mx8_decode(codes, scales, x, root: bool = False, stream=None):
 
 
 # ------------------------------------------------------- 8-bit layer operators
+# torch dtypes of the operators' tensors, filled with the first call: dtype -> ZERO_TYPE_*
+_matrix_types: dict = {}
+_code_types: set = set()
+_scale_types: set = set()
+
+
+def _fill_types():
+    import torch
+    _code_types.update(getattr(torch, k) for k in _CODES)
+    _scale_types.update(getattr(torch, k) for k in _SCALES)
+    _matrix_types.update({getattr(torch, k): v for k, v in _LIST_TYPES.items()})
+
+
+def _current() -> int:
+    """The current device, and the dtype tables filled."""
+    if not _matrix_types:
+        _fill_types()
+    return _current_device()
+
+
 def _matrix(t, what: str, cur: int) -> Matrix:
     """The C struct of a 2-D device tensor whose rows are contiguous."""
-    kind = _LIST_TYPES.get(_dtype_name(t))
+    kind, shape = _matrix_types.get(t.dtype), t.shape
     if kind is None:
         raise ValueError(f"{what}: dtype {t.dtype}, expected one of {tuple(_LIST_TYPES)}")
-    if t.dim() != 2:
-        raise ValueError(f"{what}: a 2-D tensor expected, got {t.dim()} dimensions")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if len(shape) != 2:
+        raise ValueError(f"{what}: a 2-D tensor expected, got {len(shape)} dimensions")
+    rows, cols = shape
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be neighbours")
     if t.get_device() != cur:
         _check_current(t, what, cur)
     # the strides of a single row, or of no elements, have no meaning (torch may give any)
-    return Matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 and cols else cols, kind, 0)
+    return Matrix(t.data_ptr(), rows, cols, stride if rows > 1 and cols else cols, kind)
 
 
 def _block8(codes, scales, what: str, cur: int, blocks: Optional[str] = None) -> Block8:
     """The C struct of a matrix in the 8-bit form.  The kind of its blocks
     follows from the scales' shape where it is not given (a single row has
     the same scales in both)."""
-    if _dtype_name(codes) not in _CODES or _dtype_name(scales) not in _SCALES:
+    if codes.dtype not in _code_types or scales.dtype not in _scale_types:
         raise ValueError(f"{what}: codes of {_CODES} and scales of {_SCALES} expected, got {codes.dtype} and "
                          f"{scales.dtype}")
-    if codes.dim() != 2 or scales.dim() != 2:
+    shape, sshape = codes.shape, scales.shape
+    if len(shape) != 2 or len(sshape) != 2:
         raise ValueError(f"{what}: 2-D codes and scales expected")
-    rows, cols = codes.shape
+    rows, cols = shape
+    srows, scols = sshape
     across, down = -(-cols // BLOCK8), -(-rows // BLOCK8)
-    srows = int(scales.shape[0])
-    if scales.shape[1] != across or srows not in {"rows": (rows,), "tiles": (down,), None: (rows, down)}[blocks]:
-        raise ValueError(f"{what}: scales of {tuple(scales.shape)} for codes of {tuple(codes.shape)}, expected "
+    by_rows = srows == rows if blocks is None else blocks == "rows"
+    if scols != across or srows != (rows if by_rows else down):
+        raise ValueError(f"{what}: scales of {tuple(sshape)} for codes of {tuple(shape)}, expected "
                          f"({rows} or {down}, {across}) by rows or tiles")
-    if (cols > 1 and codes.stride(1) != 1) or (across > 1 and scales.stride(1) != 1):
+    stride, inner = codes.stride()
+    sstride, sinner = scales.stride()
+    if (inner != 1 and cols > 1) or (sinner != 1 and across > 1):
         raise ValueError(f"{what}: the bytes of a row must be neighbours")
-    for t in (codes, scales):
-        if t.get_device() != cur:
-            _check_current(t, what, cur)
-    kind = BLOCKS["rows" if srows == rows else "tiles"] if blocks is None else BLOCKS[blocks]
+    if codes.get_device() != cur or scales.get_device() != cur:
+        _check_current(codes, what, cur)
+        _check_current(scales, what, cur)
     # the strides of a single row, or of no elements, have no meaning (torch may give any)
-    return Block8(codes.data_ptr(), scales.data_ptr(), rows, cols,
-                  codes.stride(0) if rows > 1 and cols else -(-cols // 16) * 16,
-                  scales.stride(0) if srows > 1 and cols else -(-across // 4) * 4, kind, 0)
+    return Block8(codes.data_ptr(), scales.data_ptr(), rows, cols, stride if rows > 1 and cols else (cols + 15) & ~15,
+                  sstride if srows > 1 and cols else (across + 3) & ~3, 0 if by_rows else 1)
 
 
 def _blocks(name: str) -> str:
@@ -768,10 +797,18 @@ def _blocks(name: str) -> str:
     return name
 
 
-def _vector(t, n: int, kinds: Sequence[str], what: str, cur: int) -> int:
-    if t.dim() != 1 or t.numel() != n:
+def _vector(t, n: int, what: str, cur: int, any_type: bool = False) -> int:
+    """The address of a contiguous device vector of n float32 (any_type: or
+    16-bit) elements."""
+    if t.shape != (n,):
         raise ValueError(f"{what}: {n} elements expected, got a tensor of {tuple(t.shape)}")
-    _check_operand(t, n, tuple(kinds), what, cur)
+    kind = _matrix_types.get(t.dtype)
+    if kind is None or not (any_type or kind == TYPE_F32):
+        raise ValueError(f"{what}: dtype {t.dtype}, expected one of {tuple(_LIST_TYPES) if any_type else 'float32'}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: tensor must be contiguous")
+    if t.get_device() != cur:
+        _check_current(t, what, cur)
     return t.data_ptr()
 
 
@@ -811,18 +848,18 @@ def block8_encode(x, codes=None, scales=None, codes_t=None, scales_t=None, block
     into the 8-bit form: ``codes`` and ``scales`` as it is, ``codes_t`` and
     ``scales_t`` transposed (either pair may be None).  ``blocks``: "rows" (128
     values along a row of the codes share a scale) or "tiles" (128 x 128)."""
-    cur = _current_device()
+    cur = _current()
     _blocks(blocks)
     mx = _matrix(x, "matrix", cur)
     if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
         raise ValueError("codes and scales come together")
     out = None if codes is None else _block8(codes, scales, "codes", cur, blocks)
     out_t = None if codes_t is None else _block8(codes_t, scales_t, "transposed codes", cur, blocks)
-    rm = None if row_mul is None else _vector(row_mul, mx.rows, ("float32",), "row multipliers", cur)
+    rm = None if row_mul is None else _vector(row_mul, mx.rows, "row multipliers", cur)
     cm, ctype = None, TYPE_NONE
     if col_mul is not None:
-        cm = _vector(col_mul, mx.cols, tuple(_LIST_TYPES), "column multipliers", cur)
-        ctype = _LIST_TYPES[_dtype_name(col_mul)]
+        cm = _vector(col_mul, mx.cols, "column multipliers", cur, True)
+        ctype = _matrix_types[col_mul.dtype]
     _check(lib().zero_block8_encode(C.byref(mx), rm, cm, ctype, _ref(out), _ref(out_t), _stream(stream)),
            "zero_block8_encode")
 
@@ -831,47 +868,47 @@ def rms_norm8(x, weight, codes, scales, rstd, residual=None, h=None, eps: float 
     """The root-mean-square norm of x (+ residual) times ``weight``, in the 8-bit
     form by rows.  ``rstd`` (float32 [rows]) and with a residual ``h`` (the sum, of
     x's dtype; may be x or residual itself) are written for the backward pass."""
-    cur = _current_device()
+    cur = _current()
     mx = _matrix(x, "x", cur)
     mr = None if residual is None else _matrix(residual, "residual", cur)
     mh = None if h is None else _matrix(h, "h", cur)
-    w = _vector(weight, mx.cols, tuple(_LIST_TYPES), "weight", cur)
-    r = _vector(rstd, mx.rows, ("float32",), "rstd", cur)
-    _check(lib().zero_rms_norm8(C.byref(mx), _ref(mr), w, _LIST_TYPES[_dtype_name(weight)], float(eps), _ref(mh),
+    w = _vector(weight, mx.cols, "weight", cur, True)
+    r = _vector(rstd, mx.rows, "rstd", cur)
+    _check(lib().zero_rms_norm8(C.byref(mx), _ref(mr), w, _matrix_types[weight.dtype], float(eps), _ref(mh),
                                 C.byref(_block8(codes, scales, "codes", cur, "rows")), r, _stream(stream)),
            "zero_rms_norm8")
 
 
 def rms_norm8_workspace_bytes(rows: int, cols: int) -> int:
-    return int(lib().zero_rms_norm8_workspace_bytes(int(rows), int(cols)))
+    return lib().zero_rms_norm8_workspace_bytes(rows, cols)
 
 
 def rms_norm8_backward(dy, h, weight, rstd, dx, dweight=None, workspace=None, dh=None, stream=None):
     """rms_norm8's gradients: ``dx`` (of x and of residual; may be dy or dh
     itself) and ``dweight`` (float32, or None).  ``h``: rms_norm8's h, or its x
     where it had no residual.  ``dh``: what reaches h another way."""
-    cur = _current_device()
+    cur = _current()
     my, mh, mx = _matrix(dy, "dy", cur), _matrix(h, "h", cur), _matrix(dx, "dx", cur)
     md = None if dh is None else _matrix(dh, "dh", cur)
-    w = _vector(weight, my.cols, tuple(_LIST_TYPES), "weight", cur)
-    r = _vector(rstd, my.rows, ("float32",), "rstd", cur)
+    w = _vector(weight, my.cols, "weight", cur, True)
+    r = _vector(rstd, my.rows, "rstd", cur)
     dw = ws = None
     if dweight is not None:
-        dw = _vector(dweight, my.cols, ("float32",), "dweight", cur)
+        dw = _vector(dweight, my.cols, "dweight", cur)
         ws = _scratch(workspace, rms_norm8_workspace_bytes(my.rows, my.cols), "workspace", cur)
-    _check(lib().zero_rms_norm8_backward(C.byref(my), C.byref(mh), w, _LIST_TYPES[_dtype_name(weight)], r, _ref(md),
+    _check(lib().zero_rms_norm8_backward(C.byref(my), C.byref(mh), w, _matrix_types[weight.dtype], r, _ref(md),
                                          C.byref(mx), dw, ws, _stream(stream)), "zero_rms_norm8_backward")
 
 
 def block8_workspace_bytes(m: int, n: int, k: int) -> int:
-    return int(lib().zero_block8_workspace_bytes(int(m), int(n), int(k)))
+    return lib().zero_block8_workspace_bytes(m, n, k)
 
 
 def block8_product(a, a_scales, b, b_scales, out, add=None, workspace=None, stream=None):
     """out = a b^T (+ add) of two matrices in the 8-bit form, [M, K] and [N, K].
     ``add``: of out's dtype and shape; may be out itself.  ``workspace``: of
     block8_workspace_bytes(M, N, K) bytes (may be None if that is 0)."""
-    cur = _current_device()
+    cur = _current()
     ma, mb = _block8(a, a_scales, "a", cur), _block8(b, b_scales, "b", cur)
     mo = _matrix(out, "out", cur)
     mc = None if add is None else _matrix(add, "add", cur)

@@ -327,49 +327,50 @@ __device__ __forceinline__ void scaled(const float (&h)[kU], float rstd, const f
 }
 
 // ------------------------------------------------------------------- norm
-// kWaves waves hold a row in registers, kNS units a lane.  Rows of one wave
-// need no barrier; kPack of them make a workgroup.  A workgroup takes rows in
-// turn, the next one's loads under way while this one is worked on, and keeps
-// its columns' weights in registers.
+// A row is held in registers, kNS units a lane, by kWaves waves; rows of one
+// wave need no barrier, and kPack of them make a workgroup.  A workgroup takes
+// rows in turn, the next one's loads under way while this one is worked on,
+// and keeps its columns' weights in registers.
 template <int kWaves>
 constexpr int kPack = kWaves == 1 ? 4 : 1;
 template <int kWaves>
 constexpr int kThreads = 64 * kWaves * kPack<kWaves>;
 
 // A vector's units of a lane.
-template <int kWaves, int kNS>
-__device__ __forceinline__ void load_weights(const void* w, int type, int c0, int n, float (&v)[kNS][kU]) {
+template <int kNS>
+__device__ __forceinline__ void load_weights(const void* w, int type, int c0, int across, int n, float (&v)[kNS][kU]) {
 #pragma unroll
-    for (int s = 0; s < kNS; ++s) load_vector(w, type, c0 + s * kWaves * kSweep, n, v[s]);
+    for (int s = 0; s < kNS; ++s) load_vector(w, type, c0 + s * across, n, v[s]);
 }
 
 // A row's units of a lane.
-template <int kType, int kWaves, int kNS>
-__device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t stride, int c0, int n,
+template <int kType, int kNS>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t stride, int c0, int across, int n,
                                          Raw<kType> (&x)[kNS]) {
     const char* from = row_of<kType>(p, row, stride);
 #pragma unroll
-    for (int s = 0; s < kNS; ++s) x[s] = load_unit<kType>(from, c0 + s * kWaves * kSweep, n);
+    for (int s = 0; s < kNS; ++s) x[s] = load_unit<kType>(from, c0 + s * across, n);
 }
 
 template <int kType, bool kRes, int kWaves, int kNS>
 __global__ __launch_bounds__(kThreads<kWaves>) void norm8_kernel(NormArgs a) {
+    constexpr int across = kWaves * kSweep;
     const int c0 = (kWaves == 1 ? threadIdx.x & 63 : threadIdx.x) * kU;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kPack<kWaves>;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kPack<kWaves> + (kWaves == 1 ? threadIdx.x >> 6 : 0);
     if (row >= a.rows) return;
     Raw<kType> nx[kNS], nr[kNS];
-    load_row<kType, kWaves>(a.x, row, a.x_stride, c0, a.cols, nx);
-    if (kRes) load_row<kType, kWaves>(a.r, row, a.r_stride, c0, a.cols, nr);
+    load_row<kType>(a.x, row, a.x_stride, c0, across, a.cols, nx);
+    if (kRes) load_row<kType>(a.r, row, a.r_stride, c0, across, a.cols, nr);
     float w[kNS][kU];
-    load_weights<kWaves>(a.w, a.w_type, c0, a.cols, w);
+    load_weights(a.w, a.w_type, c0, across, a.cols, w);
     for (int turn = 0; row < a.rows; row += step, ++turn) {
         float v[kNS][kU];
         double sum = 0.0;
         char* h = row_of<kType>(a.h, row, a.h_stride);
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
-            const int c = c0 + s * kWaves * kSweep;
+            const int c = c0 + s * across;
             if (kRes) {
                 const Raw<kType> y = add_units(nx[s], nr[s], v[s]);
                 if (c < a.cols) store_unit(h, c, a.cols, y);
@@ -379,14 +380,14 @@ __global__ __launch_bounds__(kThreads<kWaves>) void norm8_kernel(NormArgs a) {
             sum = square_sum(v[s], sum);
         }
         if (row + step < a.rows) {
-            load_row<kType, kWaves>(a.x, row + step, a.x_stride, c0, a.cols, nx);
-            if (kRes) load_row<kType, kWaves>(a.r, row + step, a.r_stride, c0, a.cols, nr);
+            load_row<kType>(a.x, row + step, a.x_stride, c0, across, a.cols, nx);
+            if (kRes) load_row<kType>(a.r, row + step, a.r_stride, c0, across, a.cols, nr);
         }
         const float rstd = rstd_of(row_sum<kWaves>(sum, turn), a.cols, a.eps);
         if (c0 == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
-            const int c = c0 + s * kWaves * kSweep;
+            const int c = c0 + s * across;
             if ((c & ~(kSweep - 1)) >= a.cols) break;  // the whole wave
             float y[kU];
             scaled(v[s], rstd, w[s], y);
@@ -459,6 +460,7 @@ __device__ __forceinline__ Raw<kType> grad_unit(const float (&g)[kU], const floa
 // registers, one row of `part` at the end.
 template <int kType, int kWaves, int kNS>
 __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBackArgs a) {
+    constexpr int across = kWaves * kSweep;
     const int c0 = (kWaves == 1 ? threadIdx.x & 63 : threadIdx.x) * kU;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kPack<kWaves>;
     const bool has_dh = a.dh != nullptr;
@@ -472,15 +474,15 @@ __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBa
     float nrstd = 0.0f;
     const auto load = [&](int64_t at) {
         if (at >= a.rows) return;
-        load_row<kType, kWaves>(a.dy, at, a.dy_stride, c0, a.cols, ny);
-        load_row<kType, kWaves>(a.h, at, a.h_stride, c0, a.cols, nh);
+        load_row<kType>(a.dy, at, a.dy_stride, c0, across, a.cols, ny);
+        load_row<kType>(a.h, at, a.h_stride, c0, across, a.cols, nh);
         nrstd = a.rstd[at];
     };
     load(row);
-    load_weights<kWaves>(a.w, a.w_type, c0, a.cols, w);
+    load_weights(a.w, a.w_type, c0, across, a.cols, w);
     for (int turn = 0; row < a.rows; row += step, ++turn) {
         const float rstd = nrstd;
-        if (has_dh) load_row<kType, kWaves>(a.dh, row, a.dh_stride, c0, a.cols, nd);
+        if (has_dh) load_row<kType>(a.dh, row, a.dh_stride, c0, across, a.cols, nd);
         float g[kNS][kU], xh[kNS][kU], sum = 0.0f;
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
@@ -498,7 +500,7 @@ __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBa
         const float c = row_sum<kWaves>(sum, turn) / static_cast<float>(a.cols);
 #pragma unroll
         for (int s = 0; s < kNS; ++s) {
-            const int at = c0 + s * kWaves * kSweep;
+            const int at = c0 + s * across;
             if (at < a.cols)
                 store_unit(row_of<kType>(a.dx, row, a.dx_stride), at, a.cols,
                            grad_unit<kType>(g[s], xh[s], c, rstd, has_dh, nd[s]));
@@ -519,7 +521,7 @@ __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBa
     }
 #pragma unroll
     for (int s = 0; s < kNS; ++s) {
-        const int c = c0 + s * kWaves * kSweep;
+        const int c = c0 + s * across;
 #pragma unroll
         for (int i = 0; i < kU; ++i)
             if (c + i < a.cols) part[c + i] = dw[s][i];
@@ -568,20 +570,21 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm8_backward_long_kernel(No
 }
 
 // dweight = the parts' sum, in float64 and a fixed order: 16 columns and 64
-// parts at a time to a workgroup.
+// parts at a time to a workgroup, then a wave for each column.
 __global__ __launch_bounds__(1024) void norm8_dweight_kernel(const float* part, int groups, int cols, float* dw) {
     __shared__ double s[64][17];
-    const int j = threadIdx.x & 15, g0 = threadIdx.x >> 4;
+    const int j = threadIdx.x & 15, g0 = threadIdx.x >> 4, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int c = blockIdx.x * 16 + j;
     double x = 0.0;
-    if (c < cols)
+    if (c < cols) {
+#pragma unroll 4
         for (int g = g0; g < groups; g += 64) x += part[static_cast<int64_t>(g) * cols + c];
+    }
     s[g0][j] = x;
     __syncthreads();
-    if (threadIdx.x >= 16 || c >= cols) return;
-    x = 0.0;
-    for (int g = 0; g < 64; ++g) x += s[g][j];
-    dw[c] = static_cast<float>(x);
+    x = row_sum<1>(s[lane][wave], 0);
+    if (lane == 0 && blockIdx.x * 16 + wave < static_cast<unsigned>(cols))
+        dw[blockIdx.x * 16 + wave] = static_cast<float>(x);
 }
 
 // ----------------------------------------------------------------- encode
@@ -755,37 +758,54 @@ void with_type(int type, F f) {
 }
 
 // Calls f with the waves and the units a lane that hold a row of n columns:
-// (0, 0) for a row too long for registers.
-template <typename F>
+// (0, 0) for a row too long for registers.  At most eight waves, two
+// workgroups of which fit a CU (4099 x 12289 fp16: 46 us in eight waves of
+// four units, 70 in nine of three, which fit once).  Rows of 1025 to 2048 are
+// faster in two waves forward (8192 x 1600 bf16 with a residual: 19.7 us; in
+// one 24.9, in four 25.2) and in one backward (24.2 us; 29.5 in two, 42.8 in
+// four).
+template <int kType, bool kBack, typename F>
 void with_row_shape(int n, F f) {
     using std::integral_constant;
+    constexpr integral_constant<int, 0> k0{};
+    constexpr integral_constant<int, 1> k1{};
+    constexpr integral_constant<int, 2> k2{};
+    constexpr integral_constant<int, 3> k3{};
+    constexpr integral_constant<int, 4> k4{};
+    constexpr integral_constant<int, 8> k8{};
     if (n <= kSweep)
-        f(integral_constant<int, 1>(), integral_constant<int, 1>());
+        f(k1, k1);
     else if (n <= 2 * kSweep)
-        f(integral_constant<int, 1>(), integral_constant<int, 2>());
+        f(k1, k2);
     else if (n <= 4 * kSweep)
-        f(integral_constant<int, 1>(), integral_constant<int, 4>());
+        f(integral_constant<int, kBack ? 1 : 2>(), integral_constant<int, kBack ? 4 : 2>());
     else if (n <= 8 * kSweep)
-        f(integral_constant<int, 4>(), integral_constant<int, 2>());
+        f(k4, k2);
+    else if (n <= 12 * kSweep)
+        f(k4, k3);
     else if (n <= 16 * kSweep)
-        f(integral_constant<int, 8>(), integral_constant<int, 2>());
-    else if (n <= 32 * kSweep)
-        f(integral_constant<int, 8>(), integral_constant<int, 4>());
+        f(k8, k2);
+    else if (n <= 24 * kSweep)
+        f(k8, k3);
+    else if (n <= 32 * kSweep && !(kBack && kType == ZERO_TYPE_F32))
+        f(k8, integral_constant<int, kBack && kType == ZERO_TYPE_F32 ? 3 : 4>());  // (backward in fp32 does not fit)
     else
-        f(integral_constant<int, 0>(), integral_constant<int, 0>());
+        f(k0, k0);
 }
 
 // Workgroups of the norm's kernels: enough rows under way to cover memory's
 // latency, few enough that each goes on to a next row.
-constexpr int kNormWavesPerCu = 16;
+constexpr int kCus = 256;  // of an MI355X; the choice costs time alone
+template <int kWaves, int kNS>
+constexpr int64_t kNormGroups = kCus * (kNS >= 3 ? 16 : 24) / (kWaves * kPack<kWaves>);
 template <int kWaves>
-constexpr int64_t kNormGroups = 256 * kNormWavesPerCu / (kWaves * kPack<kWaves>);
+constexpr int64_t kBackGroups = kCus * 8 / (kWaves * kPack<kWaves>);
 
-constexpr int kBackWavesPerCu = 8;
 template <int kWaves>
-constexpr int64_t kBackGroups = 256 * kBackWavesPerCu / (kWaves * kPack<kWaves>) < 256
-                                    ? 256
-                                    : 256 * kBackWavesPerCu / (kWaves * kPack<kWaves>);
+int64_t groups_of(int64_t rows, int64_t cap) {
+    const int64_t most = (rows + kPack<kWaves> - 1) / kPack<kWaves>;
+    return most < cap ? most : cap;
+}
 
 }  // namespace
 
@@ -795,7 +815,7 @@ int launch_norm8(const NormArgs& a, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     with_type(a.type, [&](auto type) {
         constexpr int kType = decltype(type)::value;
-        with_row_shape(a.cols, [&](auto waves, auto units) {
+        with_row_shape<kType, false>(a.cols, [&](auto waves, auto units) {
             constexpr int kWaves = decltype(waves)::value, kNS = decltype(units)::value;
             if constexpr (kWaves == 0) {
                 const unsigned grid = grid_of(a.rows);
@@ -804,8 +824,7 @@ int launch_norm8(const NormArgs& a, void* stream) {
                 else
                     norm8_long_kernel<kType, false><<<grid, kLongWaves * 64, 0, s>>>(a);
             } else {
-                const int64_t most = (a.rows - 1) / kPack<kWaves> + 1;
-                const unsigned grid = static_cast<unsigned>(most < kNormGroups<kWaves> ? most : kNormGroups<kWaves>);
+                const unsigned grid = static_cast<unsigned>(groups_of<kWaves>(a.rows, kNormGroups<kWaves, kNS>));
                 if (a.r != nullptr)
                     norm8_kernel<kType, true, kWaves, kNS><<<grid, kThreads<kWaves>, 0, s>>>(a);
                 else
@@ -822,14 +841,13 @@ int launch_norm8_backward(const NormBackArgs& a, void* stream) {
     if (a.rows > 0) {
         with_type(a.type, [&](auto type) {
             constexpr int kType = decltype(type)::value;
-            with_row_shape(a.cols, [&](auto waves, auto units) {
+            with_row_shape<kType, true>(a.cols, [&](auto waves, auto units) {
                 constexpr int kWaves = decltype(waves)::value, kNS = decltype(units)::value;
                 if constexpr (kWaves == 0) {
                     norm8_backward_long_kernel<kType><<<static_cast<unsigned>(groups), kLongWaves * 64, 0, s>>>(a);
                 } else {
-                    const int64_t most = (a.rows - 1) / kPack<kWaves> + 1;
+                    const int64_t most = groups_of<kWaves>(a.rows, kBackGroups<kWaves>);
                     groups = groups < most ? groups : most;
-                    groups = groups < kBackGroups<kWaves> ? groups : kBackGroups<kWaves>;
                     norm8_backward_kernel<kType, kWaves, kNS>
                         <<<static_cast<unsigned>(groups), kThreads<kWaves>, 0, s>>>(a);
                 }

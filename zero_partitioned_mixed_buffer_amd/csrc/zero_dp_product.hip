@@ -60,20 +60,23 @@ struct Pack {
     typedef T V __attribute__((ext_vector_type(kN), aligned(sizeof(T))));
 };
 
+template <typename T, int kN, bool kAdd>
+__device__ __forceinline__ void store_whole(T* to, const float (&v)[kN], const T* add) {
+    typedef typename Pack<T, kN>::V V;
+    V x, y = {};
+    if (kAdd) y = *reinterpret_cast<const V*>(add);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] = static_cast<T>(kAdd ? v[i] + static_cast<float>(y[i]) : v[i]);
+    *reinterpret_cast<V*>(to) = x;
+}
+
 template <typename T, int kN>
 __device__ __forceinline__ void store_run(T* to, const float (&v)[kN], const T* add, int64_t left) {
-    typedef typename Pack<T, kN>::V V;
     if (left >= kN) {
-        V x;
-        if (add != nullptr) {
-            const V y = *reinterpret_cast<const V*>(add);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) x[i] = static_cast<T>(v[i] + static_cast<float>(y[i]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < kN; ++i) x[i] = static_cast<T>(v[i]);
-        }
-        *reinterpret_cast<V*>(to) = x;
+        if (add != nullptr)
+            store_whole<T, kN, true>(to, v, add);
+        else
+            store_whole<T, kN, false>(to, v, add);
         return;
     }
 #pragma unroll
@@ -386,19 +389,28 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
     // A lane has kFN neighbouring columns of 16 rows of each of its squares.
     typedef typename Out<kType>::T T;
     const int64_t corner = n0 + wn * 32 * S::kFN;
-    if (rows_a == S::kBM && rows_b == S::kBN && a.add == nullptr && parts == 1) {
+    if (rows_a == S::kBM && rows_b == S::kBN && parts == 1) {
         // a whole tile: straight out of the registers
         T* to = static_cast<T*>(a.out) + (m0 + wm * 32 * S::kFM + g * 4) * a.out_stride + corner + r32 * S::kFN;
+        const T* add = static_cast<const T*>(a.add) + (m0 + wm * 32 * S::kFM + g * 4) * a.add_stride + corner +
+                       r32 * S::kFN;
+        const auto store = [&](auto with) {
 #pragma unroll
-        for (int i = 0; i < S::kFM; ++i)
+            for (int i = 0; i < S::kFM; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float v[S::kFN];
+                for (int e = 0; e < 16; ++e) {
+                    float v[S::kFN];
 #pragma unroll
-                for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
-                store_run<T, S::kFN>(to, v, nullptr, S::kFN);
-                to += ((e & 3) == 3 ? 5 : 1) * a.out_stride;
-            }
+                    for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
+                    store_whole<T, S::kFN, decltype(with)::value>(to, v, add);
+                    to += ((e & 3) == 3 ? 5 : 1) * a.out_stride;
+                    add += ((e & 3) == 3 ? 5 : 1) * a.add_stride;
+                }
+        };
+        if (a.add == nullptr)
+            store(std::false_type());
+        else
+            store(std::true_type());
         return;
     }
     // Else 32 rows at a time through LDS, each wave in a place of its own, so
