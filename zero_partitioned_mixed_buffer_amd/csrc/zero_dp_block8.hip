@@ -588,18 +588,15 @@ __global__ __launch_bounds__(1024) void norm8_dweight_kernel(const float* part, 
 }
 
 // ----------------------------------------------------------------- encode
-template <bool kMul>
-__device__ __forceinline__ void multiply(const EncodeArgs& a, int64_t row, const float (&w)[kU], float (&v)[kU]) {
-    if (!kMul) return;
-    const float m = a.row_mul != nullptr ? a.row_mul[row] : 1.0f;
+__device__ __forceinline__ void multiply(float m, const float (&w)[kU], float (&v)[kU]) {
 #pragma unroll
     for (int i = 0; i < kU; ++i) v[i] = (v[i] * m) * w[i];
 }
 
 template <bool kMul>
-__device__ __forceinline__ void multipliers(const EncodeArgs& a, int c, float (&w)[kU]) {
+__device__ __forceinline__ void multipliers(const EncodeArgs& a, int c, int n, float (&w)[kU]) {
     if (kMul && a.col_mul != nullptr) {
-        load_vector(a.col_mul, a.col_type, c, static_cast<int>(a.cols), w);
+        load_vector(a.col_mul, a.col_type, c, n, w);
     } else {
 #pragma unroll
         for (int i = 0; i < kU; ++i) w[i] = 1.0f;
@@ -618,8 +615,10 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(EncodeArgs a) {
         const int c = static_cast<int>(u - row * sweeps) * kSweep + (threadIdx.x & 63) * kU;
         float v[kU], w[kU];
         unpack(load_unit<kType>(row_of<kType>(a.x, row, a.x_stride), c, cols), v);
-        multipliers<kMul>(a, c, w);
-        multiply<kMul>(a, row, w, v);
+        if (kMul) {
+            multipliers<kMul>(a, c, cols, w);
+            multiply(a.row_mul == nullptr ? 1.0f : a.row_mul[row], w, v);
+        }
         emit(a.codes + row * a.codes_stride, a.scales + row * a.scales_stride, c, cols, v);
     }
 }
@@ -629,29 +628,35 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(EncodeArgs a) {
 // where a lane's 8 rows of a column are 8 neighbouring bytes.
 constexpr int kTurnStride = 144;
 
-template <int kType, bool kMul, bool kTiles>
-__global__ __launch_bounds__(256) void encode_tile_kernel(EncodeArgs a) {
-    __shared__ uint32_t top[4][kB8];
-    __shared__ __attribute__((aligned(16))) uint8_t turned[kB8 * kTurnStride];
+// kWhole: the tile has all its rows and columns (straight code, a third as long).
+template <int kType, bool kMul, bool kTiles, bool kWhole>
+__device__ __forceinline__ void encode_tile(const EncodeArgs& a, int64_t tr, int tc, uint32_t (&top)[4][kB8],
+                                            uint8_t* turned) {
     const int cols = static_cast<int>(a.cols);
-    const int across = (cols + kB8 - 1) / kB8;
-    const int64_t tiles = (a.rows + kB8 - 1) / kB8 * across;
+    const int64_t rows = a.rows;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t tr = tile / across, r0 = tr * kB8 + rg * 8;
-        const int tc = static_cast<int>(tile - tr * across), c = tc * kB8 + cg * kU;
+    const int64_t r0 = tr * kB8 + rg * 8;
+    const int c = tc * kB8 + cg * kU;
+    const int n = kWhole ? c + kU : cols;  // columns, as far as this lane can tell
+    {
         Raw<kType> raw[8];
+        float rm[8], w[kU], v[8][kU];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const bool in = r0 + j < a.rows;
-            raw[j] = load_unit<kType>(row_of<kType>(a.x, in ? r0 + j : 0, a.x_stride), c, in ? cols : 0);
+            const bool in = kWhole || r0 + j < rows;
+            raw[j] = load_unit<kType>(row_of<kType>(a.x, in ? r0 + j : 0, a.x_stride), c, in ? n : 0);
         }
-        float w[kU], v[8][kU];
-        multipliers<kMul>(a, c, w);
+        if (kMul) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                rm[j] = a.row_mul == nullptr ? 1.0f : a.row_mul[kWhole || r0 + j < rows ? r0 + j : rows - 1];
+        }
+        multipliers<kMul>(a, c, n, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             unpack(raw[j], v[j]);
-            if (r0 + j < a.rows) multiply<kMul>(a, r0 + j, w, v[j]);
+            // (rows past the end are zeros, and stay out of every scale, also under a multiplier of inf)
+            if (kMul && (kWhole || r0 + j < rows)) multiply(rm[j], w, v[j]);
         }
         uint32_t tile_byte = 0;
         if (kTiles) {
@@ -674,9 +679,9 @@ __global__ __launch_bounds__(256) void encode_tile_kernel(EncodeArgs a) {
             for (int j = 0; j < 8; ++j) {
                 const uint32_t byte = kTiles ? tile_byte : scale_byte(max16(magnitude(v[j])));
                 const int64_t row = r0 + j;
-                if (row >= a.rows) continue;
-                if (c < cols)
-                    store_codes(a.codes + row * a.codes_stride, c, cols,
+                if (!kWhole && row >= rows) continue;
+                if (kWhole || c < cols)
+                    store_codes(a.codes + row * a.codes_stride, c, n,
                                 codes4(v[j][0], v[j][1], v[j][2], v[j][3], byte),
                                 codes4(v[j][4], v[j][5], v[j][6], v[j][7], byte));
                 if (!kTiles && cg == 0) a.scales[row * a.scales_stride + tc] = static_cast<uint8_t>(byte);
@@ -708,7 +713,7 @@ __global__ __launch_bounds__(256) void encode_tile_kernel(EncodeArgs a) {
                 x[0] = codes4(v[0][i], v[1][i], v[2][i], v[3][i], byte);
                 x[1] = codes4(v[4][i], v[5][i], v[6][i], v[7][i], byte);
                 *reinterpret_cast<u32x2*>(turned + (cg * kU + i) * kTurnStride + rg * 8) = x;
-                if (!kTiles && rg == 0 && c + i < cols)
+                if (!kTiles && rg == 0 && (kWhole || c + i < cols))
                     a.scales_t[static_cast<int64_t>(c + i) * a.scales_t_stride + tr] = static_cast<uint8_t>(byte);
             }
             __syncthreads();
@@ -716,19 +721,35 @@ __global__ __launch_bounds__(256) void encode_tile_kernel(EncodeArgs a) {
             for (int p = 0; p < 4; ++p) {
                 const int k = p * 32 + (threadIdx.x >> 3), part = (threadIdx.x & 7) * 16;
                 const int64_t col = static_cast<int64_t>(tc) * kB8 + k, r = tr * kB8 + part;
-                if (col >= cols || r >= a.rows) continue;
+                if (!kWhole && (col >= cols || r >= rows)) continue;
                 const u32x4 x = *reinterpret_cast<const u32x4*>(turned + k * kTurnStride + part);
                 uint8_t* to = a.codes_t + col * a.codes_t_stride + r;
-                if (r + 16 <= a.rows) {
+                if (kWhole || r + 16 <= rows) {
                     *reinterpret_cast<u32x4*>(to) = x;
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (r + i < a.rows) to[i] = static_cast<uint8_t>(x[i / 4] >> (8 * (i & 3)));
+                        if (r + i < rows) to[i] = static_cast<uint8_t>(x[i / 4] >> (8 * (i & 3)));
                 }
             }
         }
         __syncthreads();
+    }
+}
+
+template <int kType, bool kMul, bool kTiles>
+__global__ __launch_bounds__(256) void encode_tile_kernel(EncodeArgs a) {
+    __shared__ uint32_t top[4][kB8];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kB8 * kTurnStride];
+    const int across = static_cast<int>((a.cols + kB8 - 1) / kB8);
+    const int64_t tiles = (a.rows + kB8 - 1) / kB8 * across;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t tr = tile / across;
+        const int tc = static_cast<int>(tile - tr * across);
+        if ((tr + 1) * kB8 <= a.rows && (tc + 1) * static_cast<int64_t>(kB8) <= a.cols)
+            encode_tile<kType, kMul, kTiles, true>(a, tr, tc, top, turned);
+        else
+            encode_tile<kType, kMul, kTiles, false>(a, tr, tc, top, turned);
     }
 }
 
