@@ -53,7 +53,8 @@ struct Raw {
     uint32_t w[kWords];
 };
 
-// Elements c .. c + 7 of a row of n; zeros past its end.
+// Elements c .. c + 7 of a row of n > 0; zeros past its end (loads that do not
+// depend on each other: the last element stands in for what is not there).
 template <int kType>
 __device__ __forceinline__ Raw<kType> load_unit(const char* row, int c, int n) {
     Raw<kType> x;
@@ -73,20 +74,18 @@ __device__ __forceinline__ Raw<kType> load_unit(const char* row, int c, int n) {
         }
         return x;
     }
+    uint32_t e[kU];
 #pragma unroll
-    for (int i = 0; i < Raw<kType>::kWords; ++i) x.w[i] = 0;
-    if (c >= n) return x;
-    if (kType == ZERO_TYPE_F32) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + c;
-#pragma unroll
-        for (int i = 0; i < Raw<kType>::kWords; ++i)
-            if (c + i < n) x.w[i] = p[i];
-    } else {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
-#pragma unroll
-        for (int i = 0; i < kU; ++i)
-            if (c + i < n) x.w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    for (int i = 0; i < kU; ++i) {
+        const int at = c + i < n ? c + i : n - 1;
+        e[i] = kType == ZERO_TYPE_F32 ? reinterpret_cast<const uint32_t*>(row)[at]
+                                      : reinterpret_cast<const uint16_t*>(row)[at];
     }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) e[i] = c + i < n ? e[i] : 0;
+#pragma unroll
+    for (int i = 0; i < Raw<kType>::kWords; ++i)
+        x.w[i] = kType == ZERO_TYPE_F32 ? e[i] : e[2 * i % kU] | e[(2 * i + 1) % kU] << 16;
     return x;
 }
 
@@ -522,9 +521,7 @@ __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBa
 #pragma unroll
     for (int s = 0; s < kNS; ++s) {
         const int c = c0 + s * across;
-#pragma unroll
-        for (int i = 0; i < kU; ++i)
-            if (c + i < a.cols) part[c + i] = dw[s][i];
+        if (c < a.cols) store_unit(reinterpret_cast<char*>(part), c, a.cols, pack<ZERO_TYPE_F32>(dw[s]));
     }
 }
 
@@ -643,8 +640,8 @@ __device__ __forceinline__ void encode_tile(const EncodeArgs& a, int64_t tr, int
         float rm[8], w[kU], v[8][kU];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const bool in = kWhole || r0 + j < rows;
-            raw[j] = load_unit<kType>(row_of<kType>(a.x, in ? r0 + j : 0, a.x_stride), c, in ? n : 0);
+            const int64_t row = kWhole || r0 + j < rows ? r0 + j : rows - 1;
+            raw[j] = load_unit<kType>(row_of<kType>(a.x, row, a.x_stride), c, n);
         }
         if (kMul) {
 #pragma unroll
@@ -655,8 +652,11 @@ __device__ __forceinline__ void encode_tile(const EncodeArgs& a, int64_t tr, int
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             unpack(raw[j], v[j]);
-            // (rows past the end are zeros, and stay out of every scale, also under a multiplier of inf)
-            if (kMul && (kWhole || r0 + j < rows)) multiply(rm[j], w, v[j]);
+            if (kMul) multiply(rm[j], w, v[j]);
+            if (!kWhole) {  // rows past the end stay out of every scale
+#pragma unroll
+                for (int i = 0; i < kU; ++i) v[j][i] = r0 + j < rows ? v[j][i] : 0.0f;
+            }
         }
         uint32_t tile_byte = 0;
         if (kTiles) {

@@ -432,18 +432,39 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
             *reinterpret_cast<V*>(mine + ((e >> 2) * 8 + g * 4 + (e & 3)) * kWide + r32 * S::kFN) = v;
         }
         const int p0 = wm * 32 * S::kFM + i * 32;
-        for (int r = g; r < 32; r += 2) {
-            if (p0 + r >= rows_a || left <= 0) break;
-            float v[S::kFN];
+        constexpr int kAhead = 4;  // rows whose addends are read at once
+        for (int t = 0; t < 16 && p0 + 2 * t < rows_a; t += kAhead) {
+            float v[kAhead][S::kFN];
 #pragma unroll
-            for (int j = 0; j < S::kFN; ++j) v[j] = mine[r * kWide + r32 * S::kFN + j];
-            const int64_t row = m0 + p0 + r, col = corner + r32 * S::kFN;
-            if (parts > 1)
-                store_run<float, S::kFN>(a.part + (part * a.a.rows + row) * a.b.rows + col, v, nullptr, left);
-            else
-                store_run<T, S::kFN>(static_cast<T*>(a.out) + row * a.out_stride + col, v,
-                                     a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + col,
-                                     left);
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int j = 0; j < S::kFN; ++j) v[u][j] = mine[(2 * (t + u) + g) * kWide + r32 * S::kFN + j];
+            if (a.add != nullptr && parts == 1) {
+                float y[kAhead][S::kFN];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    // (rows and columns past the end: the last ones stand in)
+                    const int p = p0 + 2 * (t + u) + g;
+                    const T* add = static_cast<const T*>(a.add) + (m0 + (p < rows_a ? p : rows_a - 1)) * a.add_stride;
+#pragma unroll
+                    for (int j = 0; j < S::kFN; ++j)
+                        y[u][j] = static_cast<float>(add[j < left ? corner + r32 * S::kFN + j : a.b.rows - 1]);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                    for (int j = 0; j < S::kFN; ++j) v[u][j] += y[u][j];
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int p = p0 + 2 * (t + u) + g;
+                if (p >= rows_a || left <= 0) continue;
+                const int64_t row = m0 + p, col = corner + r32 * S::kFN;
+                if (parts > 1)
+                    store_run<float, S::kFN>(a.part + (part * a.a.rows + row) * a.b.rows + col, v[u], nullptr, left);
+                else
+                    store_run<T, S::kFN>(static_cast<T*>(a.out) + row * a.out_stride + col, v[u], nullptr, left);
+            }
         }
     }
 }
