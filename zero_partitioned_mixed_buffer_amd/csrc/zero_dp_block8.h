@@ -33,8 +33,8 @@ constexpr int64_t kProductMaxTiles = 1 << 22;
 
 inline int64_t product_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256); }
 
-// Which of the product's kernels takes a size: few rows, or tiles of 128 x 128
-// (two workgroups to a CU), 192 x 256 or 256 x 256 (one).
+// Which of the product's kernels takes a size: few rows, or tiles of 128 x 128,
+// 192 x 256 or 256 x 256, one workgroup to a CU.
 enum ProductShape { kProductFew, kProductSmall, kProductMedium, kProductLarge };
 
 constexpr int64_t kProductCus = 256;  // of an MI355X; the choice costs time alone
@@ -53,10 +53,10 @@ inline ProductShape product_shape(int64_t m, int64_t n, bool exact) {
     if (small <= kProductCus) return kProductSmall;
     const int64_t medium = ((m + 191) / 192) * ((n + 255) / 256), large = product_tiles(m, n);
     const auto rounds = [](int64_t tiles) { return (tiles + kProductCus - 1) / kProductCus; };
-    const int64_t cost_small = (rounds(small) + 1) / 2 * (exact ? 55 : 70);
+    const int64_t cost_small = rounds(small) * (exact ? 28 : 33);
     const int64_t cost_medium = rounds(medium) * 78;
     const int64_t cost_large =
-        product_rest(large) > 0 ? large / kProductCus * 100 + (exact ? 35 : 50) : rounds(large) * 100;
+        product_rest(large) > 0 ? large / kProductCus * 100 + (exact ? 35 : 40) : rounds(large) * 100;
     if (cost_large <= cost_medium && cost_large <= cost_small) return kProductLarge;
     return cost_medium <= cost_small ? kProductMedium : kProductSmall;
 }
@@ -67,7 +67,7 @@ inline ProductShape product_shape(int64_t m, int64_t n, bool exact) {
 inline int product_parts(int64_t m, int64_t n, int64_t k) {
     const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
     if (m <= 64 || tiles > kProductCus) return 1;
-    int64_t parts = 2 * kProductCus / tiles;
+    int64_t parts = kProductCus / tiles;
     const int64_t most = k / 1024;
     parts = parts < most ? parts : most;
     if (parts < 2) return 1;

@@ -121,26 +121,27 @@ __device__ __forceinline__ uint32_t scale_offset(const ProductSide& s, int64_t r
 
 // ------------------------------------------------------------------- tiles
 // A workgroup computes kBM x kBN of out with kWM x kWN waves, each of them
-// kFM x kFN squares of 32.  Blocks of 128 k of both operands go to one of two
+// kFM x kFN squares of 32.  Blocks of 128 k of both operands go to one of kS
 // places in LDS through direct loads (16 bytes a lane, no registers), and from
-// there to registers, half a block at a time.  Everything is one step ahead
-// of the matrix instructions:
+// there to registers, half a block at a time.  Everything is ahead of the
+// matrix instructions:
 //
 //   first half of block b:   multiply it; read b's second half
 //   barrier                  (b is in registers now, b + 1 is in LDS)
-//   second half of block b:  load b + 2 over b; read b + 1's first half; multiply
+//   second half of block b:  load b + kS over b; read b + 1's first half; multiply
 //
-// so that a block has a whole block's time to come out of memory, a read half
-// a block's, and there is one barrier for 128 k.  Scales go the same way, four
-// blocks in a word of a row.
+// so that a block has kS - 1 blocks' time to come out of memory, a read half a
+// block's, and there is one barrier for 128 k.  Small tiles take more places:
+// a block's time is shorter than memory's latency there.  Scales go the same
+// way, four blocks in a word of a row.
 //
 // In LDS a row's 128 bytes are eight pieces of 16, piece q of row p at place
 // q ^ (p / 2 % 8): the rows that a read takes at one piece lie in different
 // banks.  b's rows are dealt to LDS so that the kFN squares of a lane hold
 // neighbouring columns of out, which it stores at once.
-template <int kBM_, int kBN_, int kWM_, int kWN_>
+template <int kBM_, int kBN_, int kWM_, int kWN_, int kS_>
 struct Shape {
-    static constexpr int kBM = kBM_, kBN = kBN_, kWM = kWM_, kWN = kWN_;
+    static constexpr int kBM = kBM_, kBN = kBN_, kWM = kWM_, kWN = kWN_, kS = kS_;
     static constexpr int kThreads = 64 * kWM * kWN;
     static constexpr int kFM = kBM / kWM / 32, kFN = kBN / kWN / 32;
     static constexpr int kRows = kBM + kBN;
@@ -148,6 +149,7 @@ struct Shape {
     static_assert(kThreads % 128 == 0 && kBM * 8 % kThreads == 0 && kBN * 8 % kThreads == 0, "whole loads");
     static constexpr int kScalesA = (kBM + kThreads - 1) / kThreads, kScalesB = (kBN + kThreads - 1) / kThreads;
     static constexpr int kReads = 2 * (kFM + kFN);  // LDS reads of a half block
+    static_assert(kS >= 2 && kS <= 4, "scales of two groups of four blocks are held");
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -177,19 +179,26 @@ __device__ __forceinline__ void interleave() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Waits for this wave's LDS reads and direct loads, then for the workgroup.
+// Waits for this wave's LDS reads and all but its last kFlying direct loads
+// (they end in order), then for the workgroup.
+template <int kFlying>
 __device__ __forceinline__ void arrive() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    static_assert(kFlying < 64, "the counter's width");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kFlying) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-// The tile whose first element is (m0, n0), over part `part` of k.  even and
-// odd are two objects, so that the compiler sees that loads into one do not
-// touch reads of the other.
+// The tile whose first element is (m0, n0), over part `part` of k.  The places
+// in LDS are objects of their own, so that the compiler sees that loads into
+// one do not touch reads of another (p2 and p3 may be null).
 template <typename S, int kType, bool kExact>
-__device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, int64_t m0, int64_t n0, uint8_t* even,
-                                     uint8_t* odd, uint32_t* lds_scales) {
+__device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, int64_t m0, int64_t n0, uint8_t* p0,
+                                     uint8_t* p1, uint8_t* p2, uint8_t* p3, uint32_t* lds_scales) {
+    const auto place_of = [&](auto slot) {
+        constexpr int i = decltype(slot)::value;
+        return i == 0 ? p0 : i == 1 ? p1 : i == 2 ? p2 : p3;
+    };
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::kWN, wn = wave % S::kWN;
 
@@ -225,7 +234,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
         const uint32_t k0 = static_cast<uint32_t>(block) * kB8;
         const uint32_t in = (static_cast<uint32_t>(a.k) - k0 + 15) & ~15u;
         const uint32_t back = piece >= in ? piece : 0;
-        uint8_t* const to = (decltype(slot)::value ? odd : even) + wave * 1024;
+        uint8_t* const to = place_of(slot) + wave * 1024;
 #pragma unroll
         for (int i = 0; i < S::kLoadsA; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(codes_a, (lds_ptr)(to + i * S::kThreads * 16), 16,
@@ -273,7 +282,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
             fb[kk][j] = join(*reinterpret_cast<const i32x4*>(at + (at_b ^ kk * 64) + j * 32 * kB8),
                              *reinterpret_cast<const i32x4*>(at + (at_b ^ (kk * 64 + 16)) + j * 32 * kB8));
     };
-    const auto read = [&](auto slot, auto half) { read_at(decltype(slot)::value ? odd : even, half); };
+    const auto read = [&](auto slot, auto half) { read_at(place_of(slot), half); };
     // Of half a block in registers, `left` codes of a row count, the others become zeros.
     const auto trim = [&](int left, auto half) {
         constexpr int kk = decltype(half)::value;
@@ -341,44 +350,63 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
 
     constexpr std::integral_constant<int, 0> k0{};
     constexpr std::integral_constant<int, 1> k1{};
+    constexpr std::integral_constant<int, 2> k2{};
+    constexpr std::integral_constant<int, 3> k3{};
     if (first < last) {
+        constexpr int kLoads = S::kLoadsA + S::kLoadsB;
         const bool ragged = last == blocks && (a.k & (kB8 - 1)) != 0;
         const int full = last - (ragged ? 1 : 0);
-        // Loads past the last block repeat it, into the place that nobody reads any more.
+        // Loads past the last block repeat it, into a place that nobody reads any more.
         const auto load_ahead = [&](int block, auto slot) { load(block < last ? block : last - 1, slot); };
         const auto step = [&](int block, auto slot) {
-            constexpr std::integral_constant<int, 1 - decltype(slot)::value> other{};
-            if ((block + 2 & 3) == 0 && block + 2 < last) load_scales(block + 2);
+            constexpr std::integral_constant<int, (decltype(slot)::value + 1) % S::kS> next{};
+            if ((block + S::kS & 3) == 0 && block + S::kS < last) load_scales(block + S::kS);
             read(slot, k1);
             multiply(k0);
             interleave<S, kExact, 0>();
-            arrive();
-            load_ahead(block + 2, slot);
-            read(other, k0);  // (past the last block: what is there, and not used)
+            arrive<(S::kS - 2) * kLoads>();
+            load_ahead(block + S::kS, slot);
+            read(next, k0);  // (past the last block: what is there, and not used)
             read_scales(block + 1);
             multiply(k1);
-            interleave<S, kExact, S::kLoadsA + S::kLoadsB>();
+            interleave<S, kExact, kLoads>();
             take_scales(block + 1);
         };
         load_scales(first);
         load(first, k0);
         load_ahead(first + 1, k1);
-        arrive();
+        if (S::kS > 2) load_ahead(first + 2, k2);
+        if (S::kS > 3) load_ahead(first + 3, k3);
+        arrive<(S::kS - 1) * kLoads>();
         read(k0, k0);
         read_scales(first);
         take_scales(first);
         int block = first;
-        for (; block + 1 < full; block += 2) {
+        for (; block + S::kS <= full; block += S::kS) {
             step(block, k0);
             step(block + 1, k1);
+            if (S::kS > 2) step(block + 2, k2);
+            if (S::kS > 3) step(block + 3, k3);
         }
-        if (block < full) step(block++, k0);
+        uint8_t* at = p0;  // the place of block `block`
+        if (block < full) {
+            step(block++, k0);
+            at = p1;
+            if (S::kS > 2 && block < full) {
+                step(block++, k1);
+                at = p2;
+                if (S::kS > 3 && block < full) {
+                    step(block++, k2);
+                    at = p3;
+                }
+            }
+        }
         if (ragged) {  // its first half has been read
             const int left = a.k - block * kB8;
             if (left < kB8 / 2) trim(left, k0);
             multiply(k0);
             if (left > kB8 / 2) {
-                read_at(full - first & 1 ? odd : even, k1);
+                read_at(at, k1);
                 trim(left - kB8 / 2, k1);
                 multiply(k1);
             }
@@ -419,7 +447,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
     constexpr int kHalf = S::kWM * S::kWN / 2;
     static_assert(kWide * 32 * 4 * kHalf <= S::kRows * kB8, "room for the waves' squares");
     __syncthreads();  // the last block's reads
-    float* const mine = reinterpret_cast<float*>(wave < kHalf ? even : odd) + wave % kHalf * kWide * 32;
+    float* const mine = reinterpret_cast<float*>(wave < kHalf ? p0 : p1) + wave % kHalf * kWide * 32;
     const int64_t left = a.b.rows - corner - r32 * S::kFN;
 #pragma unroll
     for (int i = 0; i < S::kFM; ++i) {
@@ -480,33 +508,38 @@ __device__ __forceinline__ void corner_of(uint32_t id, const ProductArgs& a, int
     n0 = static_cast<int64_t>(across) * wide;
 }
 
+// The places of a workgroup in LDS, each an object of its own.
+#define ZDP_PLACES(S)                                                                              \
+    __shared__ __attribute__((aligned(1024))) uint8_t place0[S::kRows * kB8];                      \
+    __shared__ __attribute__((aligned(1024))) uint8_t place1[S::kRows * kB8];                      \
+    __shared__ __attribute__((aligned(1024))) uint8_t place2[S::kS > 2 ? S::kRows * kB8 : 1];      \
+    __shared__ __attribute__((aligned(1024))) uint8_t place3[S::kS > 3 ? S::kRows * kB8 : 1];      \
+    __shared__ uint32_t lds_scales[2 * S::kRows];
+
 // The first `count` tiles of shape S.  Consecutive workgroups go to the eight
 // dies in turn; each die takes a run of neighbouring tiles, whose operands
 // then meet in its L2.
 template <typename S, int kType>
 __global__ __launch_bounds__(S::kThreads) void product_kernel(ProductArgs a, int parts, uint32_t count) {
-    __shared__ __attribute__((aligned(1024))) uint8_t even[S::kRows * kB8];
-    __shared__ __attribute__((aligned(1024))) uint8_t odd[S::kRows * kB8];
-    __shared__ uint32_t lds_scales[2 * S::kRows];
+    ZDP_PLACES(S)
     const uint32_t die = blockIdx.x & 7, more = count & 7;
     int64_t m0, n0;
     corner_of(die * (count >> 3) + (die < more ? die : more) + (blockIdx.x >> 3), a, S::kBM, S::kBN, m0, n0);
-    tile<S, kType, kType == ZERO_TYPE_F32>(a, parts, blockIdx.y, m0, n0, even, odd, lds_scales);
+    tile<S, kType, kType == ZERO_TYPE_F32>(a, parts, blockIdx.y, m0, n0, place0, place1, place2, place3, lds_scales);
 }
 
 // The tiles from `first` on of twice S's size, each as four of shape S.
 template <typename S, int kType>
 __global__ __launch_bounds__(S::kThreads) void product_rest_kernel(ProductArgs a, uint32_t first) {
-    __shared__ __attribute__((aligned(1024))) uint8_t even[S::kRows * kB8];
-    __shared__ __attribute__((aligned(1024))) uint8_t odd[S::kRows * kB8];
-    __shared__ uint32_t lds_scales[2 * S::kRows];
+    ZDP_PLACES(S)
     int64_t m0, n0;
     corner_of(first + (blockIdx.x >> 2), a, 2 * S::kBM, 2 * S::kBN, m0, n0);
     m0 += (blockIdx.x >> 1 & 1) * S::kBM;
     n0 += (blockIdx.x & 1) * S::kBN;
     if (m0 < a.a.rows && n0 < a.b.rows)
-        tile<S, kType, kType == ZERO_TYPE_F32>(a, 1, 0, m0, n0, even, odd, lds_scales);
+        tile<S, kType, kType == ZERO_TYPE_F32>(a, 1, 0, m0, n0, place0, place1, place2, place3, lds_scales);
 }
+#undef ZDP_PLACES
 
 // The parts' sum, in order, and the addend.
 template <int kType>
@@ -627,9 +660,9 @@ void launch_few(const ProductArgs& a, hipStream_t s) {
         product_few_kernel<kType, kExact, 4><<<grid, kFewWaves * 64, 0, s>>>(a);
 }
 
-typedef Shape<256, 256, 2, 4> Large;
-typedef Shape<192, 256, 2, 4> Medium;
-typedef Shape<128, 128, 2, 2> Small;
+typedef Shape<256, 256, 2, 4, 2> Large;
+typedef Shape<192, 256, 2, 4, 2> Medium;
+typedef Shape<128, 128, 2, 2, 4> Small;
 static_assert(Large::kBM == 2 * Small::kBM && Large::kBN == 2 * Small::kBN, "a large tile is four small ones");
 
 template <typename S, int kType>
