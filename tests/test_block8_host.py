@@ -61,7 +61,7 @@ def test_blocks_are_counted_from_the_first_row_and_column():
 def test_workspaces(L):
     ws = L.zero_block8_workspace_bytes
     assert ws(0, 5, 5) == ws(5, 0, 5) == ws(5, 5, 0) == ws(-1, 5, 5) == 0
-    assert ws(1, 6400, 1600) == ws(64, 6400, 100000) == 0
+    assert ws(1, 6400, 1600) == 0
     for m, n, k in ((768, 768, 32768), (65, 16, 8192), (300, 500, 2048), (2048, 2048, 1 << 23)):
         b = ws(m, n, k)
         assert b % 16 == 0 and (b == 0 or b >= 2 * m * n * 4), (m, n, k)

@@ -239,7 +239,7 @@ int64_t zero_block8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
     if (m <= 0 || n <= 0 || k <= 0 || m > kB8MaxRows || n > kB8MaxRows || k > kB8MaxCols) return 0;
     if (zdp::product_tiles(m, n) > zdp::kProductMaxTiles) return 0;
     const int parts = zdp::product_parts(m, n, k);
-    return parts > 1 ? (parts * m * n * 4 + 15) / 16 * 16 : 0;
+    return parts > 1 ? parts * zdp::product_part_rows(m) * zdp::product_part_rows(n) * 4 : 0;
 }
 
 int zero_block8_product(const zero_block8* a, const zero_block8* b, const zero_matrix* add, const zero_matrix* out,
@@ -270,6 +270,8 @@ int zero_block8_product(const zero_block8* a, const zero_block8* b, const zero_m
     p.add = add != nullptr ? add->data : nullptr;
     p.out = out->data;
     p.part = static_cast<float*>(workspace);
+    p.part_rows = zdp::product_part_rows(a->rows);
+    p.part_stride = zdp::product_part_rows(b->rows);
     p.add_stride = add != nullptr ? add->stride : 0;
     p.out_stride = out->stride;
     p.k = static_cast<int32_t>(a->cols);

@@ -33,11 +33,65 @@ constexpr int64_t kProductMaxTiles = 1 << 22;
 
 inline int64_t product_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256); }
 
-// Which of the product's kernels takes a size: few rows, or tiles of 128 x 128,
-// 192 x 256 or 256 x 256, one workgroup to a CU.
-enum ProductShape { kProductFew, kProductSmall, kProductMedium, kProductLarge };
+// Which of the product's kernels takes a size: the one without LDS on the way
+// in, with either operand as its stream, or tiles of 128 x 128, 192 x 256 or
+// 256 x 256, one workgroup to a CU.
+enum ProductShape { kProductFewB, kProductFewA, kProductSmall, kProductMedium, kProductLarge };
 
-constexpr int64_t kProductCus = 256;  // of an MI355X; the choice costs time alone
+constexpr int64_t kProductCus = 256;  // of an MI355X; the choices cost time alone
+
+inline int64_t product_small_tiles(int64_t m, int64_t n) { return ((m + 127) / 128) * ((n + 127) / 128); }
+
+// Parts that the sum over k of a product of small tiles is split into where
+// there are few of them (more than one: each part's fp32 sums go to the
+// workspace, and a second launch adds them up).
+inline int64_t product_split(int64_t tiles, int64_t k) {
+    if (tiles > kProductCus) return 1;
+    int64_t parts = kProductCus / tiles;
+    const int64_t most = k / 1024;
+    parts = parts < most ? parts : most;
+    if (parts < 2) return 1;
+    // parts begin at a multiple of four blocks; none is empty
+    const int64_t blocks = b8_blocks(k), per = ((blocks + parts - 1) / parts + 3) / 4 * 4;
+    return (blocks + per - 1) / per;
+}
+
+// Rows of the other operand that a workgroup of the kernel without LDS takes, in sixteens.
+inline int64_t product_few_rows(int64_t other) { return other <= 16 ? 1 : other <= 32 ? 2 : 4; }
+
+inline int64_t product_few_groups(int64_t stream, int64_t other) {
+    const int64_t t = product_few_rows(other);
+    return ((stream + 15) / 16) * ((other + 16 * t - 1) / (16 * t));
+}
+
+// Estimated times in ns, fitted to measurements between 1 x 1600 x 6400 and
+// 64 x 8192 x 8192.  Without LDS: 2.7 us and what a CU reads, at 40 bytes a ns
+// (70 where the other operand is short), or memory's rate.  Measured, bf16:
+// 1 x 6400 x 1600 3.8 us (in tiles 8.1), 267 x 1327 x 826 5.6 (8.9), 1034 x 165
+// x 4042 10.9 (13.7), 768 cubed 8.8 (6.1), 64 x 8192 x 8192 52 (20).
+inline int64_t product_few_ns(int64_t stream, int64_t other, int64_t k) {
+    const int64_t t = product_few_rows(other), groups = product_few_groups(stream, other);
+    const int64_t share = groups > kProductCus ? groups * 16 / kProductCus : 16;  // of a CU, in sixteenths
+    const int64_t work = share * (1 + t) * k / (t <= 2 ? 70 : 40), read = (stream + other) * k / 4500;
+    return 2700 + (work > read ? work : read);
+}
+
+// In small tiles: 4 us, 0.35 for a block of 128 k, 3 for a split, or memory's rate.
+inline int64_t product_small_ns(int64_t m, int64_t n, int64_t k) {
+    const int64_t tiles = product_small_tiles(m, n), parts = product_split(tiles, k);
+    const int64_t work = 350 * ((b8_blocks(k) + parts - 1) / parts) * ((tiles + kProductCus - 1) / kProductCus);
+    const int64_t read = (m + n) * k / 4500;
+    return 4000 + (work > read ? work : read) + (parts > 1 ? 3000 : 0);
+}
+
+// Whether the kernel without LDS takes a size (its grid has to stay one that
+// the estimate was fitted to).
+inline bool product_few(int64_t m, int64_t n, int64_t k, ProductShape* shape) {
+    const int64_t ns_a = product_few_ns(m, n, k), ns_b = product_few_ns(n, m, k);
+    *shape = ns_a < ns_b ? kProductFewA : kProductFewB;
+    return (ns_a < ns_b ? product_few_groups(m, n) : product_few_groups(n, m)) <= 4 * kProductCus &&
+           (ns_a < ns_b ? ns_a : ns_b) < product_small_ns(m, n, k);
+}
 
 // Tiles of 256 x 256 past the last full round that are taken in quarters: up
 // to one quarter to a CU.
@@ -46,14 +100,16 @@ inline int64_t product_rest(int64_t tiles) {
     return tiles > kProductCus && rest <= kProductCus / 4 ? rest : 0;
 }
 
-// By the time that the slowest CU takes, in hundredths of a 256 x 256 tile's.
-inline ProductShape product_shape(int64_t m, int64_t n, bool exact) {
-    if (m <= 64) return kProductFew;
-    const int64_t small = ((m + 127) / 128) * ((n + 127) / 128);
+// Among the tiles: by the time that the slowest CU takes, in hundredths of a
+// 256 x 256 tile's (K = 4096: small 18.8 us of 55 a round, 192 x 256 43).
+inline ProductShape product_shape(int64_t m, int64_t n, int64_t k, bool exact) {
+    ProductShape few;
+    if (product_few(m, n, k, &few)) return few;
+    const int64_t small = product_small_tiles(m, n);
     if (small <= kProductCus) return kProductSmall;
     const int64_t medium = ((m + 191) / 192) * ((n + 255) / 256), large = product_tiles(m, n);
     const auto rounds = [](int64_t tiles) { return (tiles + kProductCus - 1) / kProductCus; };
-    const int64_t cost_small = rounds(small) * (exact ? 28 : 33);
+    const int64_t cost_small = rounds(small) * (exact ? 28 : 36);
     const int64_t cost_medium = rounds(medium) * 78;
     const int64_t cost_large =
         product_rest(large) > 0 ? large / kProductCus * 100 + (exact ? 35 : 40) : rounds(large) * 100;
@@ -61,20 +117,13 @@ inline ProductShape product_shape(int64_t m, int64_t n, bool exact) {
     return cost_medium <= cost_small ? kProductMedium : kProductSmall;
 }
 
-// Parts that a product's sum over k is split into where there are few tiles
-// (more than one: each part's fp32 sums go to the workspace, and a second
-// launch adds them up).
 inline int product_parts(int64_t m, int64_t n, int64_t k) {
-    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
-    if (m <= 64 || tiles > kProductCus) return 1;
-    int64_t parts = kProductCus / tiles;
-    const int64_t most = k / 1024;
-    parts = parts < most ? parts : most;
-    if (parts < 2) return 1;
-    // parts begin at a multiple of four blocks; none is empty
-    const int64_t blocks = b8_blocks(k), per = ((blocks + parts - 1) / parts + 3) / 4 * 4;
-    return static_cast<int>((blocks + per - 1) / per);
+    ProductShape few;
+    return product_few(m, n, k, &few) ? 1 : static_cast<int>(product_split(product_small_tiles(m, n), k));
 }
+
+// The parts' sums lie in whole small tiles.
+inline int64_t product_part_rows(int64_t m) { return (m + 127) / 128 * 128; }
 
 struct NormArgs {
     const void* x;
@@ -129,8 +178,8 @@ struct ProductArgs {
     ProductSide a, b;
     const void* add;  // or null
     void* out;
-    float* part;      // [parts][m][n]
-    int64_t add_stride, out_stride;
+    float* part;      // [parts][part_rows][part_stride]: whole small tiles
+    int64_t add_stride, out_stride, part_rows, part_stride;
     int32_t k, type;
 };
 

@@ -417,22 +417,51 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
     // A lane has kFN neighbouring columns of 16 rows of each of its squares.
     typedef typename Out<kType>::T T;
     const int64_t corner = n0 + wn * 32 * S::kFN;
-    if (rows_a == S::kBM && rows_b == S::kBN && parts == 1) {
+    if (parts > 1) {
+        // the parts' sums are kept by whole tiles
+        float* to = a.part + (part * a.part_rows + m0 + wm * 32 * S::kFM + g * 4) * a.part_stride + corner + r32 * S::kFN;
+#pragma unroll
+        for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float v[S::kFN];
+#pragma unroll
+                for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
+                store_whole<float, S::kFN, false>(to, v, nullptr);
+                to += ((e & 3) == 3 ? 5 : 1) * a.part_stride;
+            }
+        return;
+    }
+    if (rows_a == S::kBM && rows_b == S::kBN) {
         // a whole tile: straight out of the registers
         T* to = static_cast<T*>(a.out) + (m0 + wm * 32 * S::kFM + g * 4) * a.out_stride + corner + r32 * S::kFN;
         const T* add = static_cast<const T*>(a.add) + (m0 + wm * 32 * S::kFM + g * 4) * a.add_stride + corner +
                        r32 * S::kFN;
         const auto store = [&](auto with) {
+            constexpr bool kAdd = decltype(with)::value;
+            constexpr int kAhead = 8;  // rows whose addends are read at once (out may be the same memory)
+            typedef typename Pack<T, S::kFN>::V V;
 #pragma unroll
             for (int i = 0; i < S::kFM; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float v[S::kFN];
+                for (int e0 = 0; e0 < 16; e0 += kAhead) {
+                    V y[kAhead];
 #pragma unroll
-                    for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
-                    store_whole<T, S::kFN, decltype(with)::value>(to, v, add);
-                    to += ((e & 3) == 3 ? 5 : 1) * a.out_stride;
-                    add += ((e & 3) == 3 ? 5 : 1) * a.add_stride;
+                    for (int e = 0; e < kAhead; ++e) {
+                        y[e] = V{};
+                        if (kAdd) y[e] = *reinterpret_cast<const V*>(add);
+                        add += ((e & 3) == 3 ? 5 : 1) * a.add_stride;
+                    }
+#pragma unroll
+                    for (int e = 0; e < kAhead; ++e) {
+                        V x;
+#pragma unroll
+                        for (int j = 0; j < S::kFN; ++j)
+                            x[j] = static_cast<T>(kAdd ? acc[i][j][e0 + e] + static_cast<float>(y[e][j])
+                                                       : acc[i][j][e0 + e]);
+                        *reinterpret_cast<V*>(to) = x;
+                        to += ((e & 3) == 3 ? 5 : 1) * a.out_stride;
+                    }
                 }
         };
         if (a.add == nullptr)
@@ -467,7 +496,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
             for (int u = 0; u < kAhead; ++u)
 #pragma unroll
                 for (int j = 0; j < S::kFN; ++j) v[u][j] = mine[(2 * (t + u) + g) * kWide + r32 * S::kFN + j];
-            if (a.add != nullptr && parts == 1) {
+            if (a.add != nullptr) {
                 float y[kAhead][S::kFN];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
@@ -488,10 +517,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
                 const int p = p0 + 2 * (t + u) + g;
                 if (p >= rows_a || left <= 0) continue;
                 const int64_t row = m0 + p, col = corner + r32 * S::kFN;
-                if (parts > 1)
-                    store_run<float, S::kFN>(a.part + (part * a.a.rows + row) * a.b.rows + col, v[u], nullptr, left);
-                else
-                    store_run<T, S::kFN>(static_cast<T*>(a.out) + row * a.out_stride + col, v[u], nullptr, left);
+                store_run<T, S::kFN>(static_cast<T*>(a.out) + row * a.out_stride + col, v[u], nullptr, left);
             }
         }
     }
@@ -541,84 +567,103 @@ __global__ __launch_bounds__(S::kThreads) void product_rest_kernel(ProductArgs a
 }
 #undef ZDP_PLACES
 
-// The parts' sum, in order, and the addend.
+// The parts' sum, in order, and the addend; a lane takes four columns.
 template <int kType>
 __global__ __launch_bounds__(256) void join_parts_kernel(ProductArgs a, int parts) {
     typedef typename Out<kType>::T T;
-    const int64_t m = a.a.rows, n = a.b.rows, across = (n + 3) / 4;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < m * across;
-         u += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = u / across, c = (u - row * across) * 4;
-        const int left = n - c < 4 ? static_cast<int>(n - c) : 4;
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int p = 0; p < parts; ++p) {
-            const float* from = a.part + (p * m + row) * n + c;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left) v[i] += from[i];
-        }
+    const uint32_t across = static_cast<uint32_t>((a.b.rows + 3) / 4);
+    const uint32_t units = static_cast<uint32_t>(a.a.rows) * across;  // (of at most 256 tiles)
+    const int64_t apart = a.part_rows * a.part_stride;
+    for (uint32_t u = blockIdx.x * 256 + threadIdx.x; u < units; u += gridDim.x * 256) {
+        const uint32_t row = u / across, c = (u - row * across) * 4;
+        const float* from = a.part + row * a.part_stride + c;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) x += *reinterpret_cast<const f32x4*>(from + p * apart);
+        const float v[4] = {x[0], x[1], x[2], x[3]};
         store_run<T, 4>(static_cast<T*>(a.out) + row * a.out_stride + c, v,
-                        a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + c, left);
+                        a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + row * a.add_stride + c,
+                        a.b.rows - c);
     }
 }
 
 // --------------------------------------------------------------- few rows
-// At most 64 rows of a (tokens), 16 kT of them: the time goes into reading b
-// once.  A workgroup takes 16 rows of b, its waves blocks of k in turn,
-// straight into registers; the waves' sums meet in LDS.  b is the
-// instruction's first operand, so that a lane holds four neighbouring columns
-// of out for one token.
+// Products whose time is latency or the reading of one operand: no LDS on the
+// way in.  A workgroup takes 16 rows of the one operand (the stream, read
+// once) against 16 kT of the other, its waves blocks of k in turn, straight
+// into registers; the waves' sums meet in LDS.  b's rows are the instruction's
+// first operand, whichever the stream is, so that a lane holds four
+// neighbouring columns of out.
 constexpr int kFewWaves = 8;
 
-template <int kType, bool kExact, int kT>
+template <int kType, bool kStreamA, int kT>
 __global__ __launch_bounds__(kFewWaves * 64) void product_few_kernel(ProductArgs a) {
+    constexpr bool kExact = kType == ZERO_TYPE_F32;
     __shared__ f32x4 sums[kFewWaves][kT][64];
+    const ProductSide& stream = kStreamA ? a.a : a.b;
+    const ProductSide& other = kStreamA ? a.b : a.a;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-    const int64_t row_b = n0 + r < a.b.rows ? n0 + r : a.b.rows - 1;
-    const uint8_t* const pb = a.b.codes + row_b * a.b.codes_stride;
-    const uint8_t* const sb = scale_row(a.b, row_b);
-    const uint8_t *pa[kT], *sa[kT];
+    const int64_t s0 = static_cast<int64_t>(blockIdx.x) * 16, t0 = static_cast<int64_t>(blockIdx.y) * 16 * kT;
+    // rows past the end repeat the last one
+    const int64_t row_s = s0 + r < stream.rows ? s0 + r : stream.rows - 1;
+    const uint8_t* const ps = stream.codes + row_s * stream.codes_stride;
+    const uint8_t* const ss = scale_row(stream, row_s);
+    const uint8_t *pt[kT], *st[kT];
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
-        const int64_t row = t * 16 + r < a.a.rows ? t * 16 + r : a.a.rows - 1;
-        pa[t] = a.a.codes + row * a.a.codes_stride;
-        sa[t] = scale_row(a.a, row);
+        const int64_t row = t0 + t * 16 + r < other.rows ? t0 + t * 16 + r : other.rows - 1;
+        pt[t] = other.codes + row * other.codes_stride;
+        st[t] = scale_row(other, row);
     }
     f32x4 acc[kT];
 #pragma unroll
     for (int t = 0; t < kT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int blocks = (a.k + kB8 - 1) / kB8;
     for (int block = wave; block < blocks; block += kFewWaves) {
-        const int k = block * kB8 + g * 32, left = a.k - k;
+        // of a row's eight pieces of 16 a lane takes g and g + 4: each load reads half rows, whole
+        const int k = block * kB8 + g * 16, left = a.k - k;
         // pieces past the row's end repeat its first
-        const int o0 = left > 0 ? k : 0, o1 = left > 16 ? k + 16 : 0;
-        i32x4 x = *reinterpret_cast<const i32x4*>(pb + o0), y = *reinterpret_cast<const i32x4*>(pb + o1);
-        const uint32_t eb = sb[block];
-        const i32x8 fb = join(keep(x, left), keep(y, left - 16));
-        i32x8 fa[kT];
-        uint32_t ea[kT];
+        const int o0 = left > 0 ? k : 0, o1 = left > 64 ? k + 64 : 0;
+        i32x4 x[2], y[kT][2];
+        uint32_t et[kT];
+        x[0] = *reinterpret_cast<const i32x4*>(ps + o0);
+        x[1] = *reinterpret_cast<const i32x4*>(ps + o1);
+        const uint32_t es = ss[block];
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
-            x = *reinterpret_cast<const i32x4*>(pa[t] + o0);
-            y = *reinterpret_cast<const i32x4*>(pa[t] + o1);
-            fa[t] = join(keep(x, left), keep(y, left - 16));
-            ea[t] = sa[t][block];
+            y[t][0] = *reinterpret_cast<const i32x4*>(pt[t] + o0);
+            y[t][1] = *reinterpret_cast<const i32x4*>(pt[t] + o1);
+            et[t] = st[t][block];
         }
+        if ((block + 1) * kB8 > a.k) {
+            x[0] = keep(x[0], left);
+            x[1] = keep(x[1], left - 64);
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+                y[t][0] = keep(y[t][0], left);
+                y[t][1] = keep(y[t][1], left - 64);
+            }
+        }
+        const i32x8 fs = join(x[0], x[1]);
         if (!kExact) {
 #pragma unroll
-            for (int t = 0; t < kT; ++t)
-                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa[t], acc[t], 0, 0, 0,
-                                                                          static_cast<int>(eb), 0,
-                                                                          static_cast<int>(ea[t]));
+            for (int t = 0; t < kT; ++t) {
+                const i32x8 ft = join(y[t][0], y[t][1]), u = kStreamA ? ft : fs, v = kStreamA ? fs : ft;
+                const int eu = static_cast<int>(kStreamA ? et[t] : es), ev = static_cast<int>(kStreamA ? es : et[t]);
+                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v, acc[t], 0, 0, 0, eu, 0, ev);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bf16x8 hb = widen(poisoned(fb[2 * j], eb), fb[2 * j + 1], scale_value(eb));
+                const bf16x8 hs = widen(poisoned(fs[2 * j], es), fs[2 * j + 1], scale_value(es));
 #pragma unroll
-                for (int t = 0; t < kT; ++t)
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        hb, widen(poisoned(fa[t][2 * j], ea[t]), fa[t][2 * j + 1], scale_value(ea[t])), acc[t], 0, 0, 0);
+                for (int t = 0; t < kT; ++t) {
+                    const i32x4 ft = y[t][j >> 1];
+                    const bf16x8 ht =
+                        widen(poisoned(ft[2 * (j & 1)], et[t]), ft[2 * (j & 1) + 1], scale_value(et[t]));
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kStreamA ? ht : hs, kStreamA ? hs : ht, acc[t], 0,
+                                                                     0, 0);
+                }
             }
         }
     }
@@ -633,7 +678,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void product_few_kernel(ProductArgs
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += x[i];
     }
-    const int64_t row = wave * 16 + r, c = n0 + g * 4;
+    const int64_t t1 = t0 + wave * 16;
+    const int64_t row = kStreamA ? s0 + r : t1 + r, c = (kStreamA ? t1 : s0) + g * 4;
     if (row >= a.a.rows || c >= a.b.rows) return;
     typedef typename Out<kType>::T T;
     store_run<T, 4>(static_cast<T*>(a.out) + row * a.out_stride + c, v,
@@ -648,16 +694,17 @@ int finish() {
     return ZERO_EHIP;
 }
 
-template <int kType>
+template <int kType, bool kStreamA>
 void launch_few(const ProductArgs& a, hipStream_t s) {
-    constexpr bool kExact = kType == ZERO_TYPE_F32;
-    const unsigned grid = static_cast<unsigned>((a.b.rows + 15) / 16);
-    if (a.a.rows <= 16)
-        product_few_kernel<kType, kExact, 1><<<grid, kFewWaves * 64, 0, s>>>(a);
-    else if (a.a.rows <= 32)
-        product_few_kernel<kType, kExact, 2><<<grid, kFewWaves * 64, 0, s>>>(a);
+    const int64_t stream = kStreamA ? a.a.rows : a.b.rows, other = kStreamA ? a.b.rows : a.a.rows;
+    const int64_t t = zdp::product_few_rows(other);
+    const dim3 grid(static_cast<unsigned>((stream + 15) / 16), static_cast<unsigned>((other + 16 * t - 1) / (16 * t)));
+    if (t == 1)
+        product_few_kernel<kType, kStreamA, 1><<<grid, kFewWaves * 64, 0, s>>>(a);
+    else if (t == 2)
+        product_few_kernel<kType, kStreamA, 2><<<grid, kFewWaves * 64, 0, s>>>(a);
     else
-        product_few_kernel<kType, kExact, 4><<<grid, kFewWaves * 64, 0, s>>>(a);
+        product_few_kernel<kType, kStreamA, 4><<<grid, kFewWaves * 64, 0, s>>>(a);
 }
 
 typedef Shape<256, 256, 2, 4, 2> Large;
@@ -681,8 +728,9 @@ void launch_tiles(const ProductArgs& a, int parts, hipStream_t s) {
 
 template <int kType>
 void launch_typed(const ProductArgs& a, int parts, hipStream_t s) {
-    switch (zdp::product_shape(a.a.rows, a.b.rows, kType == ZERO_TYPE_F32)) {
-        case zdp::kProductFew: launch_few<kType>(a, s); break;
+    switch (zdp::product_shape(a.a.rows, a.b.rows, a.k, kType == ZERO_TYPE_F32)) {
+        case zdp::kProductFewB: launch_few<kType, false>(a, s); break;
+        case zdp::kProductFewA: launch_few<kType, true>(a, s); break;
         case zdp::kProductSmall: launch_tiles<Small, kType>(a, parts, s); break;
         case zdp::kProductMedium: launch_tiles<Medium, kType>(a, parts, s); break;
         default: launch_tiles<Large, kType>(a, parts, s); break;
