@@ -712,9 +712,9 @@ int64_t zero_rms_norm8_workspace_bytes(int64_t rows, int64_t cols);
  *   out: F16 or BF16: the sum goes over the scaled 8-bit matrix instructions,
  *     which add the products of neighbouring k to fewer bits than fp32 holds:
  *     off by less than 2^-10 of the sum of their magnitudes (measured on normal
- *     data: 2^-16 of the result's size).  F32: codes are widened to bf16, which
- *     is exact, and summed in fp32, at half that rate; values below 2^-126 may
- *     read as 0 there.
+ *     data: 2^-16 of the result's size).  F32: codes are widened to bf16 under
+ *     their scale and summed in fp32, at half that rate; exact for values between
+ *     2^-126 and 2^127 (smaller ones may read as 0, larger ones as inf).
  *   workspace: device, zero_block8_workspace_bytes(M, N, K), 16-byte aligned
  *     (NULL if that is 0); its contents before and after do not matter.
  * A NaN code or scale reaches its row, or its column, of out.  The same call

@@ -156,7 +156,7 @@ def test_weight_gradient_agrees_with_differences():
         assert abs(host(layer.dw)[o, c] - diff) <= 3 * 2.0 ** -4 * mag + 1e-9
 
 
-@pytest.mark.parametrize("tokens,width,out", [(3, 300, 520), (2200, 256, 140)])
+@pytest.mark.parametrize("tokens,width,out", [(3, 300, 520), (9000, 256, 140)])
 def test_captured_layer(tokens, width, out):
     """Forward and backward in one graph (a product whose k is split among them),
     replayed on other inputs with eager work between, gives the eager results."""
@@ -297,6 +297,49 @@ def test_long_product(kind):
     keep[ends] = False
     assert bool((out[keep, 29000:29070] == rest).all())
     assert bool((out[:, :29000] == 7).all()) and bool((out[:, 29070:] == 7).all())
+
+
+@pytest.mark.parametrize("m,n", [(20, 30), (300, 200), (200, 2100)])
+def test_product_of_rows_far_apart(m, n):
+    """The longest strides: rows of codes 2^23 bytes apart, scales 2^20."""
+    k = 200
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def far(rows):
+        c = torch.full((rows, 1 << 23), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)[:, :k]
+        s = torch.full((rows, 1 << 20), 0xFF, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)[:, :2]
+        c.copy_(torch.randint(-2, 3, (rows, k), generator=g, device="cuda").float().to(c.dtype))
+        s.view(torch.uint8).fill_(127)
+        return c, s
+
+    (a, sa), (b, sb) = far(m), far(n)
+    want = a.double() @ b.double().t()
+    for kind in (torch.float32, BF):
+        out = torch.empty(m, n, dtype=kind, device="cuda")
+        B.block8_product(a, sa, b, sb, out, workspace=workspace(B.block8_workspace_bytes(m, n, k)))
+        assert torch.equal(out, want.to(kind))
+
+
+@pytest.mark.parametrize("cols", [100003, 1 << 20])
+def test_rows_longer_than_registers(cols):
+    rows = 3
+    x, r = torch.randn(rows, cols, device="cuda"), torch.randn(rows, cols, device="cuda")
+    w, dy = torch.rand(cols, device="cuda") + 0.5, 1e-3 * torch.randn(rows, cols, device="cuda")
+    c, s = B.block8_buffers(rows, cols)
+    rstd, h = torch.empty(rows, device="cuda"), torch.empty_like(x)
+    B.rms_norm8(x, w, c, s, rstd, residual=r, h=h)
+    assert torch.equal(h, x + r)
+    assert np.allclose(host(rstd), bo.rstd(host(h), 1e-6), rtol=1.1 * U)
+    codes, e = bo.encode(bo.normed(host(h), host(rstd), host(w)))
+    assert np.array_equal(raw(c), codes) and np.array_equal(raw(s), e)
+    dx, dw = torch.empty_like(x), torch.empty(cols, device="cuda")
+    B.rms_norm8_backward(dy, h, w, rstd, dx, dw, workspace(B.rms_norm8_workspace_bytes(rows, cols)))
+    want, want_w = bo.norm_backward(host(dy), host(h), host(w), host(rstd))
+    xh, gg = np.abs(host(h) * host(rstd)[:, None]), np.abs(host(dy) * host(w))
+    depth = 8 * -(-cols // 8192) + 22  # a lane's additions, six across its wave, 16 waves
+    tol = host(rstd)[:, None] * U * (3 * gg + xh * (gg * xh).mean(1, keepdims=True) * (depth + 9)) + 2 * U * np.abs(want)
+    assert (np.abs(host(dx) - want) <= tol).all()
+    assert (np.abs(host(dw) - want_w) <= (rows + 4) * U * (np.abs(host(dy)) * xh).sum(0) + U * np.abs(want_w)).all()
 
 
 # --------------------------------------------------------------- refusals
