@@ -252,6 +252,19 @@ def _check_ws(ws):
 
 
 _raw_stream = None
+_raw_stream_of = None
+
+
+def _stream_on(cur: int, stream) -> Optional[int]:
+    """_stream, where the current device is known already."""
+    global _raw_stream_of
+    if stream is None:
+        if _raw_stream_of is None:
+            import torch
+            torch.cuda.init()
+            _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: _stream(None))
+        return _raw_stream_of(cur)
+    return _stream(stream)
 
 
 def _stream(stream) -> Optional[int]:
@@ -747,48 +760,49 @@ def _current() -> int:
 
 def _matrix(t, what: str, cur: int) -> Matrix:
     """The C struct of a 2-D device tensor whose rows are contiguous."""
-    kind, shape = _matrix_types.get(t.dtype), t.shape
-    if kind is None:
-        raise ValueError(f"{what}: dtype {t.dtype}, expected one of {tuple(_LIST_TYPES)}")
-    if len(shape) != 2:
-        raise ValueError(f"{what}: a 2-D tensor expected, got {len(shape)} dimensions")
-    rows, cols = shape
-    stride, inner = t.stride()
+    kind = _matrix_types.get(t.dtype)
+    strides = t.stride()
+    if kind is None or len(strides) != 2:
+        raise ValueError(f"{what}: a 2-D tensor of one of {tuple(_LIST_TYPES)} expected, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    rows, cols = t.shape
+    stride, inner = strides
     if inner != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be neighbours")
     if t.get_device() != cur:
         _check_current(t, what, cur)
-    # the strides of a single row, or of no elements, have no meaning (torch may give any)
-    return Matrix(t.data_ptr(), rows, cols, stride if rows > 1 and cols else cols, kind)
+    if rows <= 1 or not cols:  # the strides of a single row, or of no elements, have no meaning (torch may give any)
+        stride = cols
+    return Matrix(t.data_ptr(), rows, cols, stride, kind)
 
 
 def _block8(codes, scales, what: str, cur: int, blocks: Optional[str] = None) -> Block8:
     """The C struct of a matrix in the 8-bit form.  The kind of its blocks
     follows from the scales' shape where it is not given (a single row has
     the same scales in both)."""
-    if codes.dtype not in _code_types or scales.dtype not in _scale_types:
-        raise ValueError(f"{what}: codes of {_CODES} and scales of {_SCALES} expected, got {codes.dtype} and "
-                         f"{scales.dtype}")
-    shape, sshape = codes.shape, scales.shape
-    if len(shape) != 2 or len(sshape) != 2:
-        raise ValueError(f"{what}: 2-D codes and scales expected")
-    rows, cols = shape
-    srows, scols = sshape
-    across, down = -(-cols // BLOCK8), -(-rows // BLOCK8)
+    strides, sstrides = codes.stride(), scales.stride()
+    if codes.dtype not in _code_types or scales.dtype not in _scale_types or len(strides) != 2 or len(sstrides) != 2:
+        raise ValueError(f"{what}: 2-D codes of {_CODES} and scales of {_SCALES} expected, got {codes.dtype} "
+                         f"{tuple(codes.shape)} and {scales.dtype} {tuple(scales.shape)}")
+    rows, cols = codes.shape
+    srows, across = scales.shape
     by_rows = srows == rows if blocks is None else blocks == "rows"
-    if scols != across or srows != (rows if by_rows else down):
-        raise ValueError(f"{what}: scales of {tuple(sshape)} for codes of {tuple(shape)}, expected "
-                         f"({rows} or {down}, {across}) by rows or tiles")
-    stride, inner = codes.stride()
-    sstride, sinner = scales.stride()
+    if across != (cols + 127) // 128 or srows != (rows if by_rows else (rows + 127) // 128):
+        raise ValueError(f"{what}: scales of {(srows, across)} for codes of {(rows, cols)}, expected "
+                         f"({rows} or {-(-rows // BLOCK8)}, {-(-cols // BLOCK8)}) by rows or tiles")
+    stride, inner = strides
+    sstride, sinner = sstrides
     if (inner != 1 and cols > 1) or (sinner != 1 and across > 1):
         raise ValueError(f"{what}: the bytes of a row must be neighbours")
     if codes.get_device() != cur or scales.get_device() != cur:
         _check_current(codes, what, cur)
         _check_current(scales, what, cur)
     # the strides of a single row, or of no elements, have no meaning (torch may give any)
-    return Block8(codes.data_ptr(), scales.data_ptr(), rows, cols, stride if rows > 1 and cols else (cols + 15) & ~15,
-                  sstride if srows > 1 and cols else (across + 3) & ~3, 0 if by_rows else 1)
+    if rows <= 1 or not cols:
+        stride = (cols + 15) & ~15
+    if srows <= 1 or not cols:
+        sstride = (across + 3) & ~3
+    return Block8(codes.data_ptr(), scales.data_ptr(), rows, cols, stride, sstride, 0 if by_rows else 1)
 
 
 def _blocks(name: str) -> str:
@@ -860,7 +874,7 @@ def block8_encode(x, codes=None, scales=None, codes_t=None, scales_t=None, block
     if col_mul is not None:
         cm = _vector(col_mul, mx.cols, "column multipliers", cur, True)
         ctype = _matrix_types[col_mul.dtype]
-    _check(lib().zero_block8_encode(C.byref(mx), rm, cm, ctype, _ref(out), _ref(out_t), _stream(stream)),
+    _check(lib().zero_block8_encode(C.byref(mx), rm, cm, ctype, _ref(out), _ref(out_t), _stream_on(cur, stream)),
            "zero_block8_encode")
 
 
@@ -875,7 +889,7 @@ def rms_norm8(x, weight, codes, scales, rstd, residual=None, h=None, eps: float 
     w = _vector(weight, mx.cols, "weight", cur, True)
     r = _vector(rstd, mx.rows, "rstd", cur)
     _check(lib().zero_rms_norm8(C.byref(mx), _ref(mr), w, _matrix_types[weight.dtype], float(eps), _ref(mh),
-                                C.byref(_block8(codes, scales, "codes", cur, "rows")), r, _stream(stream)),
+                                C.byref(_block8(codes, scales, "codes", cur, "rows")), r, _stream_on(cur, stream)),
            "zero_rms_norm8")
 
 
@@ -897,7 +911,7 @@ def rms_norm8_backward(dy, h, weight, rstd, dx, dweight=None, workspace=None, dh
         dw = _vector(dweight, my.cols, "dweight", cur)
         ws = _scratch(workspace, rms_norm8_workspace_bytes(my.rows, my.cols), "workspace", cur)
     _check(lib().zero_rms_norm8_backward(C.byref(my), C.byref(mh), w, _matrix_types[weight.dtype], r, _ref(md),
-                                         C.byref(mx), dw, ws, _stream(stream)), "zero_rms_norm8_backward")
+                                         C.byref(mx), dw, ws, _stream_on(cur, stream)), "zero_rms_norm8_backward")
 
 
 def block8_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -913,7 +927,7 @@ def block8_product(a, a_scales, b, b_scales, out, add=None, workspace=None, stre
     mo = _matrix(out, "out", cur)
     mc = None if add is None else _matrix(add, "add", cur)
     ws = _scratch(workspace, block8_workspace_bytes(ma.rows, mb.rows, ma.cols), "workspace", cur)
-    _check(lib().zero_block8_product(C.byref(ma), C.byref(mb), _ref(mc), C.byref(mo), ws, _stream(stream)),
+    _check(lib().zero_block8_product(C.byref(ma), C.byref(mb), _ref(mc), C.byref(mo), ws, _stream_on(cur, stream)),
            "zero_block8_product")
 
 
