@@ -352,7 +352,9 @@ __device__ __forceinline__ void scaled(const float (&h)[kU], float rstd, const f
 // A row is held in registers, kNS units a lane, by kWaves waves; rows of one
 // wave need no barrier, and kPack of them make a workgroup.  A workgroup takes
 // rows in turn, the next one's loads under way while this one is worked on,
-// and keeps its columns' weights in registers.
+// and keeps its columns' weights in registers.  Bound by memory: 8192 x 1600
+// bf16 with a residual 19.4 us, 4.7 TB/s (a copy reaches 5.2); by instructions
+// too without one, where fewer bytes go by: 4099 x 12288 fp16 37 us, 4.1 TB/s.
 template <int kWaves>
 constexpr int kPack = kWaves == 1 ? 4 : 1;
 template <int kWaves>
@@ -479,7 +481,8 @@ __device__ __forceinline__ Raw<kType> grad_unit(const float (&g)[kU], const floa
 }
 
 // As the norm's kernel; each workgroup keeps its part of dweight in
-// registers, one row of `part` at the end.
+// registers, one row of `part` at the end.  8192 x 1600 bf16 with dh 27.8 us,
+// of which 24 without dweight (4.4 TB/s); 4096 x 8192 fp32 82 and 76 (5.3).
 template <int kType, int kWaves, int kNS>
 __global__ __launch_bounds__(kThreads<kWaves>) void norm8_backward_kernel(NormBackArgs a) {
     constexpr int across = kWaves * kSweep;
@@ -623,7 +626,8 @@ __device__ __forceinline__ void multipliers(const EncodeArgs& a, int c, int n, f
     }
 }
 
-// By rows, as it is: a wave takes sweeps of 512 columns.
+// By rows, as it is: a wave takes sweeps of 512 columns (16384 x 8192 bf16: 75
+// us, 5.4 TB/s, memory's rate).
 template <int kType, bool kMul>
 __global__ __launch_bounds__(256) void encode_rows_kernel(EncodeArgs a) {
     const int cols = static_cast<int>(a.cols);
@@ -645,7 +649,9 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(EncodeArgs a) {
 
 // 128 x 128 values to a workgroup: lane group g (16 lanes) holds rows 8 g to
 // 8 g + 7, each lane 8 columns of them.  Transposed codes go through LDS,
-// where a lane's 8 rows of a column are 8 neighbouring bytes.
+// where a lane's 8 rows of a column are 8 neighbouring bytes.  16384 x 8192
+// bf16: both 117 us (4.6 TB/s), transposed alone 91 (4.4), whose stores are runs
+// of 128 bytes; 6400 x 1600 fp16 tiles, both: 11 us, launch and latency.
 constexpr int kTurnStride = 144;
 
 // The first `bytes` (less than all) of kWords words, by halves: few stores, at
