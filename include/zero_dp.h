@@ -692,7 +692,8 @@ int zero_rms_norm8(const zero_matrix* x, const zero_matrix* residual, const void
  *   dweight: device float[cols]; summed in a fixed order (the same call gives
  *     the same bits on the same GPU).  NULL: not computed, and workspace may be NULL.
  *   workspace: device, zero_rms_norm8_workspace_bytes(rows, cols), 16-byte
- *     aligned; its contents before and after do not matter.
+ *     aligned; its contents before and after do not matter, but no two calls
+ *     that may run at once share one.
  * No rows: dweight is 0.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW,
  * ZERO_EALIAS, ZERO_EHIP.
  */
@@ -716,7 +717,8 @@ int64_t zero_rms_norm8_workspace_bytes(int64_t rows, int64_t cols);
  *     their scale and summed in fp32, at half that rate; exact for values between
  *     2^-126 and 2^127 (smaller ones may read as 0, larger ones as inf).
  *   workspace: device, zero_block8_workspace_bytes(M, N, K), 16-byte aligned
- *     (NULL if that is 0); its contents before and after do not matter.
+ *     (NULL if that is 0); its contents before and after do not matter, but no
+ *     two calls that may run at once share one.
  * A NaN code or scale reaches its row, or its column, of out.  The same call
  * gives the same bits.  Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_EOVERFLOW,
  * ZERO_EALIAS, ZERO_EHIP.

@@ -407,6 +407,35 @@ def test_binding_refusals():
     refused(B.block8_buffers, 5, 5, "columns")
 
 
+def test_autograd_sees_what_is_written():
+    """A backward pass through a graph that saved a tensor which a call then wrote
+    raises, as after torch's own in-place operations."""
+    def saved(*shape):
+        w = torch.ones(shape, device="cuda", requires_grad=True)
+        a = w * 2
+        return a.detach(), (a * w).sum()
+
+    w, rstd = torch.ones(128, device="cuda"), torch.ones(64, device="cuda")
+    x, (c, s) = torch.randn(64, 128, device="cuda"), B.block8_buffers(64, 128)
+    ws = workspace(B.rms_norm8_workspace_bytes(64, 128))
+    calls = []
+    a, loss = saved(64, 128)
+    B.rms_norm8(x, w, c, s, rstd, residual=a, h=a)
+    calls.append(loss)
+    a, loss = saved(64, 128)
+    B.rms_norm8_backward(x, x.clone(), w, rstd, a, torch.empty(128, device="cuda"), ws)
+    calls.append(loss)
+    a, loss = saved(128)
+    B.rms_norm8_backward(x, x.clone(), w, rstd, torch.empty_like(x), a, ws)
+    calls.append(loss)
+    a, loss = saved(64, 64)
+    B.block8_product(c, s, c, s, a)
+    calls.append(loss)
+    for loss in calls:
+        with pytest.raises(RuntimeError):
+            loss.backward()
+
+
 def test_results_are_bytes_too():
     """uint8 tensors serve as codes and scales."""
     x = torch.randn(33, 200, device="cuda")

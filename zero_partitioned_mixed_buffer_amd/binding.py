@@ -738,6 +738,8 @@ def mx8_decode(codes, scales, x, root: bool = False, stream=None):
 
 
 # ------------------------------------------------------- 8-bit layer operators
+# Forward and backward passes are calls of their own on the caller's buffers;
+# autograd records none of them, but sees what they write (_written).
 # torch dtypes of the operators' tensors, filled with the first call: dtype -> ZERO_TYPE_*
 _matrix_types: dict = {}
 _code_types: set = set()
@@ -840,6 +842,19 @@ def _ref(x):
     return None if x is None else C.byref(x)
 
 
+_increment_version = None
+
+
+def _written(tensors):
+    """Tells autograd that a call writes these tensors, as torch's in-place
+    operations do: a backward pass that has saved one of them before raises."""
+    global _increment_version
+    if _increment_version is None:
+        from torch.autograd.graph import increment_version
+        _increment_version = increment_version
+    _increment_version(tensors)
+
+
 def block8_buffers(rows: int, cols: int, blocks: str = "rows", device=None):
     """New (codes, scales) tensors for a matrix of rows x cols in the 8-bit
     form, filled with zeros: views [rows, cols] and [rows or tiles of 128 rows,
@@ -876,6 +891,7 @@ def block8_encode(x, codes=None, scales=None, codes_t=None, scales_t=None, block
         ctype = _matrix_types[col_mul.dtype]
     _check(lib().zero_block8_encode(C.byref(mx), rm, cm, ctype, _ref(out), _ref(out_t), _stream_on(cur, stream)),
            "zero_block8_encode")
+    _written([t for t in (codes, scales, codes_t, scales_t) if t is not None])
 
 
 def rms_norm8(x, weight, codes, scales, rstd, residual=None, h=None, eps: float = 1e-6, stream=None):
@@ -891,6 +907,7 @@ def rms_norm8(x, weight, codes, scales, rstd, residual=None, h=None, eps: float 
     _check(lib().zero_rms_norm8(C.byref(mx), _ref(mr), w, _matrix_types[weight.dtype], float(eps), _ref(mh),
                                 C.byref(_block8(codes, scales, "codes", cur, "rows")), r, _stream_on(cur, stream)),
            "zero_rms_norm8")
+    _written((codes, scales, rstd) if h is None else (codes, scales, rstd, h))
 
 
 def rms_norm8_workspace_bytes(rows: int, cols: int) -> int:
@@ -900,7 +917,9 @@ def rms_norm8_workspace_bytes(rows: int, cols: int) -> int:
 def rms_norm8_backward(dy, h, weight, rstd, dx, dweight=None, workspace=None, dh=None, stream=None):
     """rms_norm8's gradients: ``dx`` (of x and of residual; may be dy or dh
     itself) and ``dweight`` (float32, or None).  ``h``: rms_norm8's h, or its x
-    where it had no residual.  ``dh``: what reaches h another way."""
+    where it had no residual.  ``dh``: what reaches h another way.  ``workspace``:
+    of rms_norm8_workspace_bytes() bytes, for dweight, not shared with a call
+    that may run at the same time."""
     cur = _current()
     my, mh, mx = _matrix(dy, "dy", cur), _matrix(h, "h", cur), _matrix(dx, "dx", cur)
     md = None if dh is None else _matrix(dh, "dh", cur)
@@ -912,6 +931,7 @@ def rms_norm8_backward(dy, h, weight, rstd, dx, dweight=None, workspace=None, dh
         ws = _scratch(workspace, rms_norm8_workspace_bytes(my.rows, my.cols), "workspace", cur)
     _check(lib().zero_rms_norm8_backward(C.byref(my), C.byref(mh), w, _matrix_types[weight.dtype], r, _ref(md),
                                          C.byref(mx), dw, ws, _stream_on(cur, stream)), "zero_rms_norm8_backward")
+    _written(dx if dweight is None else (dx, dweight))
 
 
 def block8_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -921,7 +941,8 @@ def block8_workspace_bytes(m: int, n: int, k: int) -> int:
 def block8_product(a, a_scales, b, b_scales, out, add=None, workspace=None, stream=None):
     """out = a b^T (+ add) of two matrices in the 8-bit form, [M, K] and [N, K].
     ``add``: of out's dtype and shape; may be out itself.  ``workspace``: of
-    block8_workspace_bytes(M, N, K) bytes (may be None if that is 0)."""
+    block8_workspace_bytes(M, N, K) bytes (may be None if that is 0), not shared
+    with a call that may run at the same time."""
     cur = _current()
     ma, mb = _block8(a, a_scales, "a", cur), _block8(b, b_scales, "b", cur)
     mo = _matrix(out, "out", cur)
@@ -929,6 +950,7 @@ def block8_product(a, a_scales, b, b_scales, out, add=None, workspace=None, stre
     ws = _scratch(workspace, block8_workspace_bytes(ma.rows, mb.rows, ma.cols), "workspace", cur)
     _check(lib().zero_block8_product(C.byref(ma), C.byref(mb), _ref(mc), C.byref(mo), ws, _stream_on(cur, stream)),
            "zero_block8_product")
+    _written(out)
 
 
 # ------------------------------------------------------------------ calibration
