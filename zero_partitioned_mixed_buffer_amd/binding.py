@@ -942,7 +942,9 @@ def block8_product(a, a_scales, b, b_scales, out, add=None, workspace=None, stre
     """out = a b^T (+ add) of two matrices in the 8-bit form, [M, K] and [N, K].
     ``add``: of out's dtype and shape; may be out itself.  ``workspace``: of
     block8_workspace_bytes(M, N, K) bytes (may be None if that is 0), not shared
-    with a call that may run at the same time."""
+    with a call that may run at the same time.  ``out`` in float32: sums in
+    float32; in 16 bits: twice as fast, on instructions that add eight
+    neighbouring k in fewer bits (include/zero_dp.h states the bound)."""
     cur = _current()
     ma, mb = _block8(a, a_scales, "a", cur), _block8(b, b_scales, "b", cur)
     mo = _matrix(out, "out", cur)
