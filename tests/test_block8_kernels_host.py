@@ -1,0 +1,86 @@
+"""The choice of the 8-bit product's kernel (no GPU): the tested sizes go to the
+kernels that they are meant for, and launches stay within their limits over the
+whole range of sizes.  The library's own header is compiled for the host."""
+import ctypes as C
+import os
+import random
+import subprocess
+
+import pytest
+
+import block8_cases as cases
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "zero_partitioned_mixed_buffer_amd", "csrc")
+SOURCE = """
+#include "zero_dp_block8.h"
+extern "C" {
+int shape(int64_t m, int64_t n, int64_t k, int exact) { return zdp::product_shape(m, n, k, exact != 0); }
+int64_t tiles(int64_t m, int64_t n) { return zdp::product_tiles(m, n); }
+int64_t rest(int64_t m, int64_t n) { return zdp::product_rest(zdp::product_tiles(m, n)); }
+int parts(int64_t m, int64_t n, int64_t k) { return zdp::product_parts(m, n, k); }
+int64_t few_groups(int64_t stream, int64_t other) { return zdp::product_few_groups(stream, other); }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def H(tmp_path_factory):
+    at = tmp_path_factory.mktemp("choice")
+    src, lib = at / "choice.cpp", at / "choice.so"
+    src.write_text(SOURCE)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-I", CSRC, "-I", os.path.join(ROOT, "include"),
+                    str(src), "-o", str(lib)], check=True)
+    h = C.CDLL(str(lib))
+    i64 = C.c_int64
+    h.shape.argtypes, h.tiles.argtypes, h.rest.argtypes = [i64, i64, i64, C.c_int], [i64, i64], [i64, i64]
+    h.parts.argtypes, h.few_groups.argtypes = [i64, i64, i64], [i64, i64]
+    for f in (h.tiles, h.rest, h.few_groups):
+        f.restype = i64
+    return h
+
+
+@pytest.mark.parametrize("case", cases.PRODUCTS + cases.MASKED + cases.EMPTY + cases.FAR)
+def test_tested_sizes_reach_their_kernels(H, case):
+    kernel, quarters, parts, m, n, k = case
+    for exact in (0, 1):
+        assert H.shape(m, n, k, exact) == kernel
+    assert (kernel == cases.LARGE and H.rest(m, n) > 0) == quarters
+    assert H.parts(m, n, k) == parts
+
+
+def test_every_kernel_has_sizes():
+    for group in (cases.PRODUCTS,):
+        assert {c[0] for c in group} == {cases.FEW_B, cases.FEW_A, cases.SMALL, cases.MEDIUM, cases.LARGE}
+    for group in (cases.MASKED, cases.EMPTY, cases.FAR):
+        assert {c[0] for c in group} == {cases.SMALL, cases.MEDIUM, cases.LARGE}
+    assert any(c[0] == cases.LARGE and not c[1] for c in cases.PRODUCTS)
+
+
+def test_launches_stay_within_their_limits(H):
+    """Random sizes over the whole range: fewer than 2^32 lanes to a launch (and
+    65536 groups along its second axis), parts for small tiles alone, none of
+    them empty, and as many quarters as there are CUs at most."""
+    g = random.Random(1)
+    size = {cases.SMALL: (128, 128, 256), cases.MEDIUM: (192, 256, 512), cases.LARGE: (256, 256, 512)}
+    seen = set()
+    for _ in range(200000):
+        m, n = (int(2 ** g.uniform(0, 30.99)) for _ in range(2))
+        k = int(2 ** g.uniform(0, 23))
+        if H.tiles(m, n) > 1 << 22:
+            continue
+        for exact in (0, 1):
+            shape, parts = H.shape(m, n, k, exact), H.parts(m, n, k)
+            seen.add(shape)
+            if shape in size:
+                bm, bn, threads = size[shape]
+                tiles = -(-m // bm) * -(-n // bn)
+                assert tiles * threads * parts < 1 << 32, (m, n, k)
+                assert parts == 1 or (shape == cases.SMALL and tiles * parts <= 256)
+                blocks = -(-k // 128)
+                per = (-(-blocks // parts) + 3) // 4 * 4
+                assert (parts - 1) * per < blocks and 0 <= H.rest(m, n) <= 64
+            else:
+                stream, other = (n, m) if shape == cases.FEW_B else (m, n)
+                assert parts == 1 and H.few_groups(stream, other) <= 1024
+    assert seen == {cases.FEW_B, cases.FEW_A, cases.SMALL, cases.MEDIUM, cases.LARGE}

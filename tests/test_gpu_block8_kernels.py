@@ -1,10 +1,12 @@
 """The 8-bit product's sums and kernels on the GPU: what its 16-bit outputs are
-off by, at the ends of the codes' range and over long k."""
+off by, at the ends of the codes' range and over long k; and each of its kernels
+(block8_cases.py) on whole numbers, bit for bit."""
 import numpy as np
 import pytest
 
+import block8_cases as cases
 from oracle import block8_oracle as bo
-from test_gpu_block8 import DT, HALF, LEAST, Guarded, _ints, _ws, host, raw
+from test_gpu_block8 import DT, HALF, LEAST, Guarded, _ws
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -82,3 +84,156 @@ def test_sums_over_long_k(m, n, k, kind):
             codes = [c | (g.integers(0, 2, c.shape) * 128).astype(np.uint8) for c in codes]
         es = [g.integers(112, 116, (r, bo.blocks_of(k))).astype(np.uint8) for r in (m, n)]
         check_sums(*(on_device(c, e) for c, e in zip(codes, es)), k, kind)
+
+
+# ------------------------------------------------------- every kernel, exactly
+KINDS = ["f32", "f16", "bf16"]
+
+
+def random(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def bytes_of(t):
+    return t.view(torch.uint8)
+
+
+def ints(g, rows, cols, tiles):
+    """Small whole numbers under scales of 1/2 to 2, and their values: products
+    and sums are exact in the instructions' arithmetic and in fp32."""
+    c, s = B.block8_buffers(rows, cols, "tiles" if tiles else "rows")
+    c.copy_(torch.randint(-4, 5, (rows, cols), generator=g, device="cuda").float())
+    bytes_of(s).copy_(torch.randint(126, 129, s.shape, generator=g, device="cuda"))
+    return c, s, values_of(c, s)
+
+
+def values_of(c, s):
+    scale = torch.exp2(bytes_of(s).double() - 127)
+    if s.shape[0] != c.shape[0]:
+        scale = scale.repeat_interleave(128, 0)[:c.shape[0]]
+    return c.double() * scale.repeat_interleave(128, 1)[:, :c.shape[1]]
+
+
+def same(got, want):
+    """Equal, NaN where NaN."""
+    return bool(((got == want) | (got.isnan() & want.isnan())).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", cases.PRODUCTS)
+def test_every_kernel_is_exact(case, kind):
+    """Into a buffer whose other bytes are checked, with and without an addend,
+    and in its place; out's rows start on 16 bytes or on an element."""
+    m, n, k = case[3:]
+    g = random(m + n + k)
+    for tiles, lead in (((False, True), 16), ((True, False), 3)):
+        a, sa, av = ints(g, m, k, tiles[0])
+        b, sb, bv = ints(g, n, k, tiles[1])
+        want = av @ bv.t()
+        add = torch.randint(-8, 9, (m, n), generator=g, device="cuda").to(DT[kind])
+        summed = (want + add.double()).to(DT[kind])
+        want = want.to(DT[kind])
+        out = Guarded(m, n, DT[kind], lead=lead)
+        ws = _ws(m, n, k)
+        B.block8_product(a, sa, b, sb, out.view, workspace=ws)
+        assert torch.equal(out.view, want)
+        B.block8_product(a, sa, b, sb, out.view, add=add, workspace=ws)
+        assert torch.equal(out.view, summed)
+        out.view.copy_(add)
+        B.block8_product(a, sa, b, sb, out.view, add=out.view, workspace=ws)
+        assert torch.equal(out.view, summed)
+        out.check()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("case", cases.MASKED)
+def test_tiles_with_nothing_between_rows_and_with_nan(case, kind):
+    """Bytes past a row's end are NaN codes and scales, and have no effect; a NaN
+    code reaches its row or column of out, a NaN scale those of its block."""
+    m, n, k = case[3:]
+    for tiles in (False, True):
+        g = random(k)
+        a, sa, av = ints(g, m, k, False)
+        b, sb, bv = ints(g, n, k, tiles)
+        for t, width in ((a, k), (b, k), (sa, 2), (sb, 2)):
+            box = bytes_of(t)
+            gap = t.stride(0) - width
+            assert gap > 0
+            nan = 0x7F if t.dtype == a.dtype else 0xFF
+            box.as_strided((t.shape[0], gap), (t.stride(0), 1), t.storage_offset() + width).fill_(nan)
+        out = torch.empty(m, n, dtype=DT[kind], device="cuda")
+        want = (av @ bv.t()).to(DT[kind])
+        B.block8_product(a, sa, b, sb, out)
+        assert torch.equal(out, want)
+        for row, col in ((3, k - 1), (m - 1, 0), (m // 2, 127)):
+            bytes_of(a)[row, col] = 0x7F
+            want[row] = float("nan")
+        for row, block in ((7, 0), (m - 2, 1)):  # over whole codes
+            bytes_of(sa)[row, block] = 0xFF
+            want[row] = float("nan")
+        bytes_of(b)[5, 0] = 0xFF
+        want[:, 5] = float("nan")
+        bytes_of(sb)[2, 1] = 0xFF
+        want[:, 256:384 if tiles else 2] = float("nan")
+        if not tiles:
+            want[:, 2] = float("nan")
+        B.block8_product(a, sa, b, sb, out)
+        assert same(out, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", cases.EMPTY)
+def test_tiles_over_no_k(case, kind):
+    m, n, k = case[3:]
+    (a, sa), (b, sb) = B.block8_buffers(m, k), B.block8_buffers(n, k)
+    out = Guarded(m, n, DT[kind])
+    B.block8_product(a, sa, b, sb, out.view)
+    assert bool((out.view == 0).all())
+    add = torch.randn(m, n, generator=random(1), device="cuda").to(DT[kind])
+    B.block8_product(a, sa, b, sb, out.view, add=add)
+    assert torch.equal(out.view, add)
+    out.check()
+
+
+@pytest.mark.parametrize("case", cases.FAR)
+def test_tiles_of_rows_far_apart(case):
+    """The longest strides of codes and of scales: offsets within a tile pass 2^31."""
+    m, n, k = case[3:]
+    assert m == n
+    c = torch.empty(m, 1 << 23, dtype=torch.uint8, device="cuda")[:, :k].view(torch.float8_e4m3fn)
+    s = torch.empty(m, 1 << 23, dtype=torch.uint8, device="cuda")[:, :bo.blocks_of(k)].view(torch.float8_e8m0fnu)
+    near = ints(random(9), m, k, False)
+    bytes_of(c).copy_(bytes_of(near[0]))
+    bytes_of(s).copy_(bytes_of(near[1]))
+    want = near[2] @ near[2].t()
+    for kind in ("f32", "bf16"):
+        out = torch.empty(m, n, dtype=DT[kind], device="cuda")
+        B.block8_product(c, s, c, s, out, workspace=_ws(m, n, k))
+        assert torch.equal(out, want.to(DT[kind]))
+    del c, s
+    torch.cuda.empty_cache()
+
+
+def test_captured_large_tiles():
+    """Large tiles, a last round in quarters and an addend in one graph, replayed
+    with other codes and eager work between."""
+    m, n, k = 4100, 4100, 700
+    g = random(4)
+    a, sa, _ = ints(g, m, k, False)
+    b, sb, _ = ints(g, n, k, True)
+    add = torch.ones(m, n, device="cuda", dtype=torch.bfloat16)
+    out = torch.empty_like(add)
+    B.block8_product(a, sa, b, sb, out, add=add)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.block8_product(a, sa, b, sb, out, add=add)
+    for seed in range(3):
+        new = ints(random(10 + seed), m, k, False)
+        bytes_of(a).copy_(bytes_of(new[0]))
+        bytes_of(sa).copy_(bytes_of(new[1]))
+        out.fill_(-1)
+        graph.replay()
+        want = (new[2] @ values_of(b, sb).t() + 1).to(out.dtype)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
