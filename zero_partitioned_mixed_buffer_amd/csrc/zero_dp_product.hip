@@ -202,6 +202,14 @@ __device__ __forceinline__ void arrive() {
     asm volatile("" ::: "memory");
 }
 
+// Between lanes of one wave that pass values through LDS: what was written
+// before is there afterwards, and what is read before is not overwritten.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The tile whose first element is (m0, n0), over part `part` of k.  The places
 // in LDS are objects of their own, so that the compiler sees that loads into
 // one do not touch reads of another (p2 and p3 may be null).
@@ -501,6 +509,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
             for (int j = 0; j < S::kFN; ++j) v[j] = acc[i][j][e];
             *reinterpret_cast<V*>(mine + ((e >> 2) * 8 + g * 4 + (e & 3)) * kWide + r32 * S::kFN) = v;
         }
+        wave_exchange();
         const int p0 = wm * 32 * S::kFM + i * 32;
         constexpr int kAhead = 4;  // rows whose addends are read at once
         for (int t = 0; t < 16 && p0 + 2 * t < rows_a; t += kAhead) {
@@ -533,6 +542,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, int parts, int part, 
                 store_run<T, S::kFN>(static_cast<T*>(a.out) + row * a.out_stride + col, v[u], nullptr, left);
             }
         }
+        wave_exchange();
     }
 }
 
