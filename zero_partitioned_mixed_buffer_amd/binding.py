@@ -738,8 +738,11 @@ def mx8_decode(codes, scales, x, root: bool = False, stream=None):
 
 
 # ------------------------------------------------------- 8-bit layer operators
-# Forward and backward passes are calls of their own on the caller's buffers;
-# autograd records none of them, but sees what they write (_written).
+# Forward and backward passes are calls of their own on the caller's buffers.
+# Autograd records none of them, so a tensor that requires a gradient is refused
+# where torch records (its gradient would be missing without a word); inside an
+# autograd.Function or torch.no_grad() nothing is recorded and all are taken.
+# Autograd sees what the calls write (_written).
 # torch dtypes of the operators' tensors, filled with the first call: dtype -> ZERO_TYPE_*
 _matrix_types: dict = {}
 _code_types: set = set()
@@ -751,6 +754,20 @@ def _fill_types():
     _code_types.update(getattr(torch, k) for k in _CODES)
     _scale_types.update(getattr(torch, k) for k in _SCALES)
     _matrix_types.update({getattr(torch, k): v for k, v in _LIST_TYPES.items()})
+
+
+_grad_enabled = None
+
+
+def _refuse_grad(t, what: str):
+    """For a tensor that requires a gradient: raises where torch records."""
+    global _grad_enabled
+    if _grad_enabled is None:
+        import torch
+        _grad_enabled = torch.is_grad_enabled
+    if _grad_enabled():
+        raise ValueError(f"{what}: the tensor requires a gradient, and autograd does not record this call; pass its "
+                         "detach(), or call in torch.no_grad() or from an autograd.Function")
 
 
 def _current() -> int:
@@ -773,6 +790,8 @@ def _matrix(t, what: str, cur: int) -> Matrix:
         raise ValueError(f"{what}: the elements of a row must be neighbours")
     if t.get_device() != cur:
         _check_current(t, what, cur)
+    if t.requires_grad:
+        _refuse_grad(t, what)
     if rows <= 1 or not cols:  # the strides of a single row, or of no elements, have no meaning (torch may give any)
         stride = cols
     return Matrix(t.data_ptr(), rows, cols, stride, kind)
@@ -799,6 +818,8 @@ def _block8(codes, scales, what: str, cur: int, blocks: Optional[str] = None) ->
     if codes.get_device() != cur or scales.get_device() != cur:
         _check_current(codes, what, cur)
         _check_current(scales, what, cur)
+    if codes.requires_grad or scales.requires_grad:
+        _refuse_grad(codes, what)
     # the strides of a single row, or of no elements, have no meaning (torch may give any)
     if rows <= 1 or not cols:
         stride = (cols + 15) & ~15
@@ -825,6 +846,8 @@ def _vector(t, n: int, what: str, cur: int, any_type: bool = False) -> int:
         raise ValueError(f"{what}: tensor must be contiguous")
     if t.get_device() != cur:
         _check_current(t, what, cur)
+    if t.requires_grad:
+        _refuse_grad(t, what)
     return t.data_ptr()
 
 
@@ -876,7 +899,11 @@ def block8_encode(x, codes=None, scales=None, codes_t=None, scales_t=None, block
     """A float32, float16 or bfloat16 matrix, or x * row_mul[:, None] * col_mul,
     into the 8-bit form: ``codes`` and ``scales`` as it is, ``codes_t`` and
     ``scales_t`` transposed (either pair may be None).  ``blocks``: "rows" (128
-    values along a row of the codes share a scale) or "tiles" (128 x 128)."""
+    values along a row of the codes share a scale) or "tiles" (128 x 128).
+
+    Autograd does not record this call or the norm and product below: where it
+    would have to (grad mode on, a tensor that requires a gradient) they raise
+    ValueError."""
     cur = _current()
     _blocks(blocks)
     mx = _matrix(x, "matrix", cur)
