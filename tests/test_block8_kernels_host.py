@@ -57,6 +57,27 @@ def test_every_kernel_has_sizes():
     assert any(c[0] == cases.LARGE and not c[1] for c in cases.PRODUCTS)
 
 
+# us in small, medium and large tiles, an MI355X: (fp32 out, m, n, k)
+MEASURED = {
+    (0, 2048, 4800, 1600): (30.3, 27.0, 26.4), (0, 4096, 2304, 768): (18.5, 14.5, 14.2),
+    (0, 4096, 4800, 768): (32.6, 28.1, 30.3), (0, 8192, 768, 768): (13.5, 14.3, 12.8),
+    (0, 8192, 1600, 4096): (73.8, 73.1, 52.4), (0, 8192, 4800, 4096): (217.4, 159.5, 167.0),
+    (0, 5333, 3500, 768): (35.0, 28.8, 31.2), (0, 6400, 6400, 768): (56.8, 49.4, 46.3),
+    (0, 11000, 2000, 1600): (60.3, 44.7, 49.9), (1, 2900, 2900, 4096): (98.7, 73.8, 84.0),
+    (1, 4096, 4800, 768): (49.9, 42.4, 43.7), (1, 8192, 768, 4096): (64.1, 63.9, 76.2),
+    (1, 8192, 4800, 768): (110.1, 83.0, 86.2), (1, 8192, 4800, 4096): (348.4, 302.0, 294.0),
+    (1, 16384, 1600, 768): (72.3, 62.0, 57.3), (1, 16384, 1600, 4096): (245.2, 226.9, 196.4),
+    (1, 6400, 6400, 1600): (165.0, 139.8, 132.3), (1, 11000, 2000, 768): (59.6, 45.5, 51.2),
+}
+
+
+@pytest.mark.parametrize("at", MEASURED)
+def test_choice_of_tiles_is_near_the_fastest(H, at):
+    exact, m, n, k = at
+    us = MEASURED[at]
+    assert us[H.shape(m, n, k, exact) - cases.SMALL] <= 1.09 * min(us)
+
+
 def test_launches_stay_within_their_limits(H):
     """Random sizes over the whole range: fewer than 2^32 lanes to a launch (and
     65536 groups along its second axis), parts for small tiles alone, none of

@@ -101,7 +101,12 @@ inline int64_t product_rest(int64_t tiles) {
 }
 
 // Among the tiles: by the time that the slowest CU takes, in hundredths of a
-// 256 x 256 tile's (K = 4096: small 18.8 us of 55 a round, 192 x 256 43).
+// 256 x 256 tile's (K = 4096: small 18.8 us of 55 a round, 192 x 256 43; fp32
+// out: 33 of 84, 74).  All three measured over 15 sizes between 2048 x 4800 and
+// 16384 x 1600: from K = 768 up the choice is the fastest of them or within 8 %
+// of it (5333 x 3500 x 768 bf16 31.2 us large, 28.8 medium); at K = 256, where
+// loads and stores weigh more than rounds, within 26 % (4096 x 4800 bf16: 23.2
+// large, 18.5 medium).
 inline ProductShape product_shape(int64_t m, int64_t n, int64_t k, bool exact) {
     ProductShape few;
     if (product_few(m, n, k, &few)) return few;
@@ -109,7 +114,7 @@ inline ProductShape product_shape(int64_t m, int64_t n, int64_t k, bool exact) {
     if (small <= kProductCus) return kProductSmall;
     const int64_t medium = ((m + 191) / 192) * ((n + 255) / 256), large = product_tiles(m, n);
     const auto rounds = [](int64_t tiles) { return (tiles + kProductCus - 1) / kProductCus; };
-    const int64_t cost_small = rounds(small) * (exact ? 28 : 36);
+    const int64_t cost_small = rounds(small) * 36;
     const int64_t cost_medium = rounds(medium) * 78;
     const int64_t cost_large =
         product_rest(large) > 0 ? large / kProductCus * 100 + (exact ? 35 : 40) : rounds(large) * 100;
