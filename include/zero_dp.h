@@ -718,10 +718,13 @@ int64_t zero_rms_norm8_workspace_bytes(int64_t rows, int64_t cols);
  *     magnitudes, every factor (zeros too) counted as at least 2^-6 of its scale,
  *     the smallest normal code: 2^-10 up to K = 8192.  Where products cancel that
  *     may be more than the result's own rounding.  (Measured on normal data: 2^-16
- *     of the result's size.)  F32: codes are widened to bf16 under their scale and
- *     summed in fp32, at half that rate; exact for values between 2^-126 and 2^127
- *     (smaller ones may read as 0, larger ones as inf).  A caller that wants
- *     sums in fp32 and 16 bits out takes F32 and rounds.
+ *     of the result's size.)  Products of few rows, or of little work, sum as F32
+ *     does, and over those instructions only where a scale byte is below
+ *     10 or above 246.
+ *     F32: codes are widened to bf16 under their scale and summed in fp32, at half
+ *     that rate; exact for values between 2^-126 and 2^127 (smaller ones may read
+ *     as 0, larger ones as inf).  A caller that wants sums in fp32 and 16 bits out
+ *     for a product of any size takes F32 and rounds.
  *   workspace: device, zero_block8_workspace_bytes(M, N, K), 16-byte aligned
  *     (NULL if that is 0); its contents before and after do not matter, but no
  *     two calls that may run at once share one.

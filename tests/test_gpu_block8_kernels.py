@@ -15,6 +15,38 @@ B = pytest.importorskip("zero_partitioned_mixed_buffer_amd.binding")
 F32, F64 = np.float32, np.float64
 
 
+KINDS = ["f32", "f16", "bf16"]
+
+
+def random(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def bytes_of(t):
+    return t.view(torch.uint8)
+
+
+def ints(g, rows, cols, tiles):
+    """Small whole numbers under scales of 1/2 to 2, and their values: products
+    and sums are exact in the instructions' arithmetic and in fp32."""
+    c, s = B.block8_buffers(rows, cols, "tiles" if tiles else "rows")
+    c.copy_(torch.randint(-4, 5, (rows, cols), generator=g, device="cuda").float())
+    bytes_of(s).copy_(torch.randint(126, 129, s.shape, generator=g, device="cuda"))
+    return c, s, values_of(c, s)
+
+
+def values_of(c, s):
+    scale = torch.exp2(bytes_of(s).double() - 127)
+    if s.shape[0] != c.shape[0]:
+        scale = scale.repeat_interleave(128, 0)[:c.shape[0]]
+    return c.double() * scale.repeat_interleave(128, 1)[:, :c.shape[1]]
+
+
+def same(got, want):
+    """Equal, NaN where NaN."""
+    return bool(((got == want) | (got.isnan() & want.isnan())).all())
+
+
 # ------------------------------------------------------- sums of 16-bit outputs
 def sum_bound(k):
     """Of the sum of the products' magnitudes, each factor counted as at least
@@ -86,39 +118,47 @@ def test_sums_over_long_k(m, n, k, kind):
         check_sums(*(on_device(c, e) for c, e in zip(codes, es)), k, kind)
 
 
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("case", [c for c in cases.PRODUCTS if c[0] in (cases.FEW_A, cases.FEW_B)])
+def test_small_products_sum_in_fp32(case, kind):
+    """Of every eight k two products of 2^16 cancel: the others are whole numbers far
+    below them, which fp32 holds beside them (2^18 units of 1/4 and more are 20
+    bits) and the 8-bit instructions do not."""
+    m, n, k = case[3:]
+    g = random(m)
+    a, sa, _ = ints(g, m, k, False)
+    b, sb, _ = ints(g, n, k, True)
+    for t, signs in ((a, (256.0, 256.0)), (b, (256.0, -256.0))):
+        for i in range(2):
+            t[:, i:k - k % 8:8] = torch.full((), signs[i], device="cuda").to(t.dtype)
+    want = (values_of(a, sa) @ values_of(b, sb).t()).to(DT[kind])
+    out = torch.empty(m, n, dtype=DT[kind], device="cuda")
+    B.block8_product(a, sa, b, sb, out)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("ea,eb", [(1, 253), (1, 200), (9, 245), (10, 244), (127, 127), (244, 10), (246, 8), (247, 7),
+                                   (254, 0), (250, 4)])
+@pytest.mark.parametrize("m,n,k", [(20, 40, 200), (130, 20, 600)])
+def test_scales_at_the_ends_of_the_range(m, n, k, ea, eb, kind):
+    """Whole numbers under the smallest and largest scale bytes, whose product is
+    ordinary: exact, in fp32 for values that bf16 holds."""
+    if kind == "f32" and not (10 <= ea <= 246 and 10 <= eb <= 246):
+        return  # may read as 0 or inf
+    g = random(k)
+    a, sa, _ = ints(g, m, k, False)
+    b, sb, _ = ints(g, n, k, False)
+    bytes_of(sa).fill_(ea)
+    bytes_of(sb).fill_(eb)
+    out = torch.empty(m, n, dtype=DT[kind], device="cuda")
+    B.block8_product(a, sa, b, sb, out)
+    want = (a.double() @ b.double().t()) * 2.0 ** (ea + eb - 254)
+    assert torch.equal(out, want.to(DT[kind]))
+
+
 # ------------------------------------------------------- every kernel, exactly
-KINDS = ["f32", "f16", "bf16"]
-
-
-def random(seed):
-    return torch.Generator(device="cuda").manual_seed(seed)
-
-
-def bytes_of(t):
-    return t.view(torch.uint8)
-
-
-def ints(g, rows, cols, tiles):
-    """Small whole numbers under scales of 1/2 to 2, and their values: products
-    and sums are exact in the instructions' arithmetic and in fp32."""
-    c, s = B.block8_buffers(rows, cols, "tiles" if tiles else "rows")
-    c.copy_(torch.randint(-4, 5, (rows, cols), generator=g, device="cuda").float())
-    bytes_of(s).copy_(torch.randint(126, 129, s.shape, generator=g, device="cuda"))
-    return c, s, values_of(c, s)
-
-
-def values_of(c, s):
-    scale = torch.exp2(bytes_of(s).double() - 127)
-    if s.shape[0] != c.shape[0]:
-        scale = scale.repeat_interleave(128, 0)[:c.shape[0]]
-    return c.double() * scale.repeat_interleave(128, 1)[:, :c.shape[1]]
-
-
-def same(got, want):
-    """Equal, NaN where NaN."""
-    return bool(((got == want) | (got.isnan() & want.isnan())).all())
-
-
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("case", cases.PRODUCTS)
 def test_every_kernel_is_exact(case, kind):

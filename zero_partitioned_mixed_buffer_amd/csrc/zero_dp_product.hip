@@ -10,12 +10,13 @@
 // normal ones counts with their smallest exponent there); the eights' sums are
 // added in fp32.  This is the choice for 16-bit outputs, which it gives at twice
 // the rate: on normal data it moves a result by 2^-16 of its size, far less than
-// the codes' own rounding did and than the output's does (error against float64:
-// 1.6689e-3 of the norm in bf16, 1.6688e-3 with sums in fp32).  Its bound, 7 *
+// the codes' own rounding did and than the output's does (8192 x 6400 x 1600
+// bf16: 1.6626e-3 of the norm against float64, 1.6625e-3 with sums in fp32).  Its bound, 7 *
 // 2^-13 of the products' magnitudes, is not that small where they cancel, or
 // where a group's largest factors are subnormal codes (measured: up to 3.4e-3 of
-// the magnitudes).  fp32 outputs widen the codes to bf16 (exact, the scale with
-// them) and take the bf16 instructions, at half the rate.
+// the magnitudes).  fp32 outputs, and products whose time is not the
+// instructions', widen the codes to bf16 (exact, the scale with them) and take
+// the bf16 instructions, at half the rate.
 //
 // The order in which an instruction takes its k does not matter as long as
 // both operands have the same, which leaves the layouts in LDS free.
@@ -616,9 +617,19 @@ __global__ __launch_bounds__(256) void join_parts_kernel(ProductArgs a, int part
 // once) against 16 kT of the other, its waves blocks of k in turn, straight
 // into registers; the waves' sums meet in LDS.  b's rows are the instruction's
 // first operand, whichever the stream is, so that a lane holds four
-// neighbouring columns of out.  1 x 6400 x 1600 bf16: 4.1 us (2.5 TB/s, of
+// neighbouring columns of out.  1 x 6400 x 1600 bf16: 4.5 us (2.3 TB/s, of
 // which 2 to 3 us are a launch's own); 8 x 8192 x 8192: 17 us, 3.9 TB/s.
+//
+// The matrix instructions' rate bounds little of it, so sums are in fp32 for every
+// type of out, over the bf16 instructions, at 0 to 10 % (1 x 6400 x 1600: 4.3 us
+// over the 8-bit ones; 267 x 1327 x 826: 5.8 and 5.5; 1034 x 165 x 4042: 11.7 and
+// 10.8; 8 x 8192 x 8192: 17.1 and 16.9).  A 16-bit out takes the 8-bit ones for a block with a
+// scale whose values bf16 does not hold.
 constexpr int kFewWaves = 8;
+
+// Whether bf16 holds every e4m3 value under a scale byte: 2^-9 at 10 is 2^-126,
+// 448 at 246 is 1.75 * 2^127.
+__device__ __forceinline__ bool fits_bf16(uint32_t byte) { return (byte >= 10u && byte <= 246u) || byte == 255u; }
 
 template <int kType, bool kStreamA, int kT>
 __global__ __launch_bounds__(kFewWaves * 64) void product_few_kernel(ProductArgs a) {
@@ -669,7 +680,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void product_few_kernel(ProductArgs
             }
         }
         const i32x8 fs = join(x[0], x[1]);
-        if (!kExact) {
+        bool fits = fits_bf16(es);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) fits = fits && fits_bf16(et[t]);
+        if (!kExact && !__all(fits)) {
 #pragma unroll
             for (int t = 0; t < kT; ++t) {
                 const i32x8 ft = join(y[t][0], y[t][1]), u = kStreamA ? ft : fs, v = kStreamA ? fs : ft;
