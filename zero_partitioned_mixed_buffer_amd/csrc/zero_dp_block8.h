@@ -67,8 +67,10 @@ inline int64_t product_few_groups(int64_t stream, int64_t other) {
 // Estimated times in ns, fitted to measurements between 1 x 1600 x 6400 and
 // 64 x 8192 x 8192.  Without LDS: 2.7 us and what a CU reads, at 40 bytes a ns
 // (70 where the other operand is short), or memory's rate.  Measured, bf16:
-// 1 x 6400 x 1600 3.8 us (in tiles 8.1), 267 x 1327 x 826 5.6 (8.9), 1034 x 165
-// x 4042 10.9 (13.7), 768 cubed 8.8 (6.1), 64 x 8192 x 8192 52 (20).
+// 1 x 6400 x 1600 4.9 us (in tiles 8.5), 267 x 1327 x 826 6.2 (8.9), 1034 x 165
+// x 4042 12.2 (14.7), 768 cubed 9.4 (6.5), 64 x 8192 x 8192 46 (22).  Over 60
+// random sizes all three choices were timed: the one taken costs 2 % more than
+// the fastest on average, 29 % at most (1526 x 462 x 1372: tiles 12.5 us, 9.7).
 inline int64_t product_few_ns(int64_t stream, int64_t other, int64_t k) {
     const int64_t t = product_few_rows(other), groups = product_few_groups(stream, other);
     const int64_t share = groups > kProductCus ? groups * 16 / kProductCus : 16;  // of a CU, in sixteenths

@@ -354,7 +354,8 @@ __device__ __forceinline__ void scaled(const float (&h)[kU], float rstd, const f
 // rows in turn, the next one's loads under way while this one is worked on,
 // and keeps its columns' weights in registers.  Bound by memory: 8192 x 1600
 // bf16 with a residual 19.4 us, 4.7 TB/s (a copy reaches 5.2); by instructions
-// too without one, where fewer bytes go by: 4099 x 12288 fp16 37 us, 4.1 TB/s.
+// too without one, where fewer bytes go by: 4099 x 12288 fp16 35 us, 4.3 TB/s (one
+// column more, a unit more for every lane: 45).
 template <int kWaves>
 constexpr int kPack = kWaves == 1 ? 4 : 1;
 template <int kWaves>
@@ -651,7 +652,8 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(EncodeArgs a) {
 // 8 g + 7, each lane 8 columns of them.  Transposed codes go through LDS,
 // where a lane's 8 rows of a column are 8 neighbouring bytes.  16384 x 8192
 // bf16: both 117 us (4.6 TB/s), transposed alone 91 (4.4), whose stores are runs
-// of 128 bytes; 6400 x 1600 fp16 tiles, both: 11 us, launch and latency.
+// of 128 bytes; 6400 x 1600 fp16 tiles, both: 11 us, launch and latency, and 650
+// tiles where registers let 512 onto the card at once.
 constexpr int kTurnStride = 144;
 
 // The first `bytes` (less than all) of kWords words, by halves: few stores, at
@@ -845,10 +847,12 @@ void with_type(int type, F f) {
 // Calls f with the waves and the units a lane that hold a row of n columns:
 // (0, 0) for a row too long for registers.  At most eight waves, two
 // workgroups of which fit a CU (4099 x 12289 fp16: 46 us in eight waves of
-// four units, 70 in nine of three, which fit once).  Rows of 1025 to 2048 are
-// faster in two waves forward (8192 x 1600 bf16 with a residual: 19.7 us; in
-// one 24.9, in four 25.2) and in one backward (24.2 us; 29.5 in two, 42.8 in
-// four).
+// four units, 70 in nine of three, which fit once).  Rows of 1025 to 2048 in
+// bf16 are faster in two waves forward (8192 x 1600 with a residual: 19.9 us; in
+// one 25.1, in four 22.0) and in one backward (27.6 us; 34.1 in two, 45.7 in
+// four), at 1032, 1280, 1536, 1792 and 2048 columns too (four waves within 1 % at
+// 1536 and 2048 forward).  In fp32 that choice is not the fastest: 8192 x 1600
+// takes 38.1 us forward (36.1 in four) and 53.7 backward (47.9 in two).
 template <int kType, bool kBack, typename F>
 void with_row_shape(int n, F f) {
     using std::integral_constant;

@@ -148,11 +148,14 @@ __device__ __forceinline__ uint32_t scale_offset(const ProductSide& s, int64_t r
 // neighbouring columns of out, which it stores at once.
 //
 // Bound by the matrix instructions at the clock that real data allow: 8192 x
-// 8192 x 8192 bf16 in 256 x 256 tiles 388 us, 2840 TFLOP/s (busy 73 % of the
-// cycles; eight waves read 192 KB of LDS a block, four of 128 x 128 would read
-// 128 KB at the same rate, but have no second wave to hide an epilogue behind);
-// fp32 out 1300.  Short k pays for each round's first loads and last stores:
-// 8192 x 6400 x 1600 bf16 85 us, 1970 TFLOP/s.
+// 8192 x 8192 bf16 in 256 x 256 tiles 402 us, 2740 TFLOP/s, on operands that the
+// caches hold, 438 us on three pairs in turn (busy 73 % of the cycles; eight
+// waves read 192 KB of LDS a block, four of 128 x 128 would read 128 KB at the
+// same rate, but have no second wave to hide an epilogue behind); fp32 out 810 us,
+// 1360.  Short k pays for each round's first loads and last stores: 8192 x 6400
+// x 1600 bf16 96 us, 1740 TFLOP/s, of which 88 in the large tiles and 11 in the
+// launch of the last 32 in quarters; 8192 x 1600 x 6400 79 us, 2120, its last
+// column of tiles three quarters empty.
 template <int kBM_, int kBN_, int kWM_, int kWN_, int kS_>
 struct Shape {
     static constexpr int kBM = kBM_, kBN = kBN_, kWM = kWM_, kWN = kWN_, kS = kS_;
